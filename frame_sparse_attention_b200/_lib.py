@@ -64,7 +64,8 @@ EXPORTS = ("sfa_error_string", "sfa_version", "sfa_set_max_count", "sfa_build_se
            "sfa_lse_merge", "sfa_hsa_max_count", "sfa_hsa_workspace", "sfa_hsa_select", "sfa_forward_blocks",
            "sfa_forward_blocks_split", "sfa_forward_blocks_split_workspace", "sfa_forward_split_plan",
            "sfa_forward_host_workspace", "sfa_forward_host", "sfa_hsa_pool_keys", "sfa_hsa_select_pooled",
-           "sfa_forward_dual_workspace", "sfa_forward_dual", "sfa_gdn_workspace", "sfa_gdn_forward")
+           "sfa_forward_dual_workspace", "sfa_forward_dual", "sfa_gdn_workspace", "sfa_gdn_forward",
+           "sfa_qk_norm_rope", "sfa_cache_write", "sfa_cache_append", "sfa_cache_read")
 
 
 def load():
@@ -136,6 +137,11 @@ def load():
                                      vp, vp]
     lib.sfa_forward_blocks.restype = st
     lib.sfa_forward_blocks.argtypes = [ctypes.POINTER(AttnDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    # descriptors of the 8-bit frame cache (see _cache.py) go by address
+    for name, n in (("sfa_qk_norm_rope", 8), ("sfa_cache_write", 7), ("sfa_cache_append", 12), ("sfa_cache_read", 7)):
+        fn = getattr(lib, name)
+        fn.restype = st
+        fn.argtypes = [vp] * (n + 1)
     _lib = lib
     return lib
 

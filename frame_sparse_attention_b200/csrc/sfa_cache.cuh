@@ -1,0 +1,126 @@
+// The 8-bit frame cache: where a token lies, and the row format (e4m3 codes in blocks of 32
+// elements, one power of two per block).
+#pragma once
+
+#include <cstdint>
+
+#include "sfa.h"
+
+namespace sfa {
+
+constexpr int CACHE_BLOCK = SFA_CACHE_BLOCK;
+constexpr int E_MIN = -124, E_MAX = 119;  // 2^-9 * 2^-124 is the smallest bf16 number, 448 * 2^119 is finite in bf16
+
+// Device view of a cache (sfa_cache without its host-only checks).
+struct CacheView {
+    uint8_t *k, *v, *k_scale, *v_scale;
+    const int32_t *table;
+    int64_t ts0, ts1;  // table strides: batch, key head
+    int32_t n_pages, heads, page_len, table_len;
+};
+
+inline CacheView cache_view(const sfa_cache *c)
+{
+    CacheView w;
+    w.k = static_cast<uint8_t *>(c->k);
+    w.v = static_cast<uint8_t *>(c->v);
+    w.k_scale = static_cast<uint8_t *>(c->k_scale);
+    w.v_scale = static_cast<uint8_t *>(c->v_scale);
+    w.table = c->table;
+    w.ts0 = c->table_stride[0];
+    w.ts1 = c->table_stride[1];
+    w.n_pages = c->n_pages;
+    w.heads = c->heads;
+    w.page_len = c->page_len;
+    w.table_len = c->table_len;
+    return w;
+}
+
+inline sfa_status check_cache(const sfa_cache *c, int32_t H_kv, int32_t d)
+{
+    if (!c) return SFA_ERR_INVALID_ARG;
+    if (c->d != 64 && c->d != 128) return SFA_ERR_UNSUPPORTED;
+    if (c->d != d || c->n_pages < 1 || c->page_len < 1 || c->table_len < 1) return SFA_ERR_INVALID_ARG;
+    if (c->heads != 1 && c->heads != H_kv) return SFA_ERR_INVALID_ARG;
+    if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->table) return SFA_ERR_INVALID_ARG;
+    const uintptr_t sb = d / CACHE_BLOCK;
+    if (reinterpret_cast<uintptr_t>(c->k) % 16 || reinterpret_cast<uintptr_t>(c->v) % 16 ||
+        reinterpret_cast<uintptr_t>(c->k_scale) % sb || reinterpret_cast<uintptr_t>(c->v_scale) % sb ||
+        reinterpret_cast<uintptr_t>(c->table) % 4)
+        return SFA_ERR_INVALID_ARG;
+    if (c->table_stride[0] < 0 || c->table_stride[1] < 0) return SFA_ERR_INVALID_ARG;
+    // a logical token is an int32, and so is a table offset times page_len
+    if ((int64_t)c->table_len * c->page_len >= ((int64_t)1 << 31)) return SFA_ERR_INVALID_ARG;
+    return SFA_OK;
+}
+
+// Strides (batch, head, token) of a [B][heads][L][d] bf16 tensor whose rows are moved 16
+// bytes at a time; the stride of a dimension of one entry is not used.
+inline bool rows_stride_ok(const int64_t *s, int64_t B, int64_t heads, int64_t L)
+{
+    const int64_t n[3] = {B, heads, L};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (s[i] <= 0 || s[i] % 8 || s[i] >= ((int64_t)1 << 38))) return false;
+    return true;
+}
+
+__device__ __forceinline__ void report_status(int32_t *status, int32_t code)
+{
+    if (status) atomicCAS(status, 0, code);
+}
+
+// Pool row of logical token j of (b, h), or -1 where it has no valid place.
+__device__ __forceinline__ int64_t cache_row(const CacheView &c, int b, int h, int64_t j)
+{
+    if (j < 0 || j >= (int64_t)c.table_len * c.page_len) return -1;
+    const uint32_t slot = (uint32_t)j / (uint32_t)c.page_len;
+    const int page = __ldg(c.table + b * c.ts0 + h * c.ts1 + slot);
+    if (page < 0 || page >= c.n_pages) return -1;
+    return ((int64_t)page * c.heads + (c.heads > 1 ? h : 0)) * c.page_len + ((uint32_t)j - slot * (uint32_t)c.page_len);
+}
+
+// e of a block whose largest magnitude has the bf16 bits `amax` (finite, sign cleared): the
+// smallest e with amax <= 448 * 2^e = 1.75 * 2^(e + 8).  For amax = (1 + m / 128) * 2^E that
+// is E - 8, one more where m > 96; adding 31 carries into the exponent field exactly then.
+__device__ __forceinline__ int block_exponent(uint32_t amax)
+{
+    const int e = (int)((amax + 31u) >> 7) - (127 + 8);
+    return min(max(e, E_MIN), E_MAX);
+}
+
+// (code of lo, code of hi) in bits [0, 8) and [8, 16): nearest even, saturated to 448
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Codes to bf16.  Each 16-bit half of x holds one code twice (byte permutation of the caller);
+// moving its exponent and mantissa to bf16's places gives the code's value times 2^(7 - 127),
+// e4m3 subnormals becoming bf16 subnormals, and the product with 2^(120 + e) is exact.
+__device__ __forceinline__ uint32_t spread_codes(uint32_t x)
+{
+    return (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
+}
+
+// bf16 bits of 2^(120 + e); 2^127 for e > 7, the rest being scale_rest's
+__device__ __forceinline__ uint32_t scale_bits(uint32_t scale_byte)
+{
+    return min(scale_byte + 120u, 254u) << 7;
+}
+// bf16 bits of 2^max(e - 7, 0)
+__device__ __forceinline__ uint32_t scale_rest_bits(uint32_t scale_byte)
+{
+    return (scale_byte > 134u ? scale_byte - 7u : 127u) << 7;
+}
+constexpr uint32_t SCALE_ONE_STEP = 134;  // scale bytes up to this need no second product
+
+}  // namespace sfa

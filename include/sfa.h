@@ -11,7 +11,9 @@
  *
  * plus variants of the forward (host buffers, paged caches, split-KV, two branches in one
  * launch), the hierarchical block selection of Light Forcing (sfa_hsa_select +
- * sfa_forward_blocks) and ARL2's inter-frame gated-delta branch (sfa_gdn_forward).
+ * sfa_forward_blocks), ARL2's inter-frame gated-delta branch (sfa_gdn_forward) and the
+ * 8-bit frame cache with what a layer does around it (sfa_qk_norm_rope, sfa_cache_write,
+ * sfa_cache_append, sfa_cache_read, sfa_forward_cache).
  *
  * Conventions
  *   - A video has T latent frames of P tokens each; token i belongs to frame i / P.
@@ -470,6 +472,107 @@ sfa_status sfa_gdn_forward(const sfa_gdn_desc *desc, const void *q, const void *
                            const float *alpha, const float *beta, const float *state_in, float *state_out,
                            void *o, int32_t update, void *workspace, size_t workspace_bytes,
                            int32_t *dev_status, sfa_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * 8-bit frame cache: norm and rotation of queries and keys, writing, reading, attention
+ * ------------------------------------------------------------------------------------
+ * ("Head Forcing", §2: every head keeps its own cache of frames; "ISPA", §1: the cache of
+ *  a streaming model is its largest tensor.)  A cache is a pool of pages of page_len rows
+ * and a page table per (batch entry, key head): logical token j of (b, h) lies in row
+ * j % page_len of page table[b * table_stride[0] + h * table_stride[1] + j / page_len].
+ * A page is a frame (page_len = P) or any other number of tokens.
+ *
+ * Row format.  The d elements of a key or value row are cut into blocks of 32.  A block
+ * holds e4m3 codes c and one power of two 2^e, its values being c * 2^e: e is the smallest
+ * exponent in [-124, 119] with max |x| <= 448 * 2^e, and c = x * 2^-e rounded to nearest
+ * even (saturated to 448).  e4m3 is a floating format, so a power-of-two scale costs no
+ * precision, and c * 2^e is a bf16 number exactly: reading back adds no rounding, and the
+ * attention sees the cache's own values.  A NaN is stored as 0 and an infinity as the
+ * largest value of its sign, and both are reported as SFA_ERR_INVALID_ARG in dev_status.
+ */
+#define SFA_CACHE_BLOCK 32
+
+typedef struct {
+    int32_t n_pages;   /* pages of the pool, >= 1                                          */
+    int32_t heads;     /* heads of a page: H_kv (the heads share a page's number), or 1 (a
+                          page belongs to one head, so that heads can keep different frames) */
+    int32_t page_len;  /* rows of a page, >= 1                                             */
+    int32_t d;         /* 64 or 128                                                        */
+    void *k, *v;             /* e4m3 codes [n_pages][heads][page_len][d], contiguous, 16-byte aligned */
+    void *k_scale, *v_scale; /* e + 127 as uint8 [n_pages][heads][page_len][d / 32], contiguous,
+                                aligned to d / 32 bytes                                    */
+    const int32_t *table;    /* device page numbers, see table_stride                      */
+    int32_t table_len;       /* entries of a table row, >= 1                               */
+    int64_t table_stride[2]; /* batch, key head (in entries; 0: the row is shared)         */
+} sfa_cache;
+
+/* Rotary positions.  The first R = 2 * sum(axis_pairs) elements of a row are rotated in R/2
+ * pairs, pair p by the angle positions[b][i][a] * inv_freq[p], a being the axis that p falls
+ * into (axis_pairs[0] pairs of axis 0, then those of axis 1, ...), and multiplied by `scale`:
+ *   (x, y) -> scale * (x cos - y sin, y cos + x sin).
+ * The angle is formed and reduced in 64 bits.  The other elements are left as they are. */
+typedef enum {
+    SFA_ROPE_INTERLEAVED = 0, /* pair p = elements (2p, 2p + 1)                             */
+    SFA_ROPE_HALF = 1         /* pair p = elements (p, p + R/2); R a multiple of 16         */
+} sfa_rope_layout;
+
+#define SFA_ROPE_MAX_AXES 4
+
+typedef struct {
+    const double *inv_freq;    /* device, R/2 entries                                      */
+    const int32_t *positions;  /* device, entry a of token i of batch entry b at
+                                  b * pos_stride[0] + i * pos_stride[1] + a                */
+    int64_t pos_stride[2];
+    int32_t layout;            /* sfa_rope_layout                                          */
+    int32_t n_axes;            /* 1 .. SFA_ROPE_MAX_AXES                                   */
+    int32_t axis_pairs[SFA_ROPE_MAX_AXES]; /* >= 0; R <= d                                 */
+    float scale;               /* finite; 1 unless a long-context scaling asks for another  */
+} sfa_rope;
+
+/* New tokens of a layer: q [B][H][L][d], k and v [B][H_kv][L][d], bf16, d contiguous,
+ * strides (batch, head, token) in elements, multiples of 8, bases 16-byte aligned.  H is a
+ * multiple of H_kv where both are used. */
+typedef struct {
+    int32_t B, H, H_kv, L, d;
+    float eps;                 /* >= 0: RMS norm of every head's row; < 0: no norm          */
+    int64_t q_stride[3], k_stride[3], v_stride[3];
+    int64_t q_out_stride[3], k_out_stride[3], v_out_stride[3];
+    int64_t start_stride[2];   /* of `start`: batch, key head (0: shared)                  */
+} sfa_rows_desc;
+
+/*
+ * Norm and rotation of queries and keys in one pass:
+ *   y = x / sqrt(mean(x^2) + eps) * weight  (per head row; weight fp32 [d] or NULL = ones;
+ *   no norm with eps < 0), then the rotation (rope NULL: none), in fp32, rounded to bf16 once.
+ * q or k may be NULL (with its output).  q_out / k_out may be q / k themselves (same strides).
+ */
+sfa_status sfa_qk_norm_rope(const sfa_rows_desc *desc, const sfa_rope *rope, const void *q, const void *k,
+                            const float *q_weight, const float *k_weight, void *q_out, void *k_out,
+                            sfa_stream_t stream);
+
+/*
+ * Write the L new keys and values of every (b, h) at logical tokens start[b][h] + i.
+ *   start  device int32 (strides in the descriptor).
+ *   lens   device int32 [B] or NULL (= L): rows i >= lens[b] are skipped (padded batches).
+ * A token whose place lies outside the table, or whose page number outside the pool, is
+ * skipped and reported as SFA_ERR_BAD_SET in dev_status.  Two tokens with the same place:
+ * either may win, per 8 elements.
+ */
+sfa_status sfa_cache_write(const sfa_rows_desc *desc, const sfa_cache *cache, const void *k, const void *v,
+                           const int32_t *start, const int32_t *lens, int32_t *dev_status, sfa_stream_t stream);
+
+/* sfa_qk_norm_rope and sfa_cache_write of its keys in one pass, without writing the bf16
+ * keys: the same q_out and cache bits as the two calls (rows i >= lens[b] of q_out are left
+ * as they are). */
+sfa_status sfa_cache_append(const sfa_rows_desc *desc, const sfa_rope *rope, const sfa_cache *cache, const void *q,
+                            const void *k, const void *v, const float *q_weight, const float *k_weight, void *q_out,
+                            const int32_t *start, const int32_t *lens, int32_t *dev_status, sfa_stream_t stream);
+
+/* Logical tokens start[b][h] + i, i < min(L, lens[b]), back as bf16 (exactly) into k_out and
+ * v_out [B][H_kv][L][d]; other rows, and tokens without a valid place (reported as
+ * SFA_ERR_BAD_SET), are left as they are. */
+sfa_status sfa_cache_read(const sfa_rows_desc *desc, const sfa_cache *cache, const int32_t *start,
+                          const int32_t *lens, void *k_out, void *v_out, int32_t *dev_status, sfa_stream_t stream);
 
 /* ------------------------------------------------------------------------------------
  * LSE merge

@@ -1,0 +1,177 @@
+"""Refusals of the 8-bit frame cache calls: on the host, before any launch (CPU)."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def sfa():
+    import os
+
+    import frame_sparse_attention_b200 as sfa
+    from frame_sparse_attention_b200 import build
+    if not os.path.exists(build.LIB):
+        build.build()
+    sfa.load()
+    return sfa
+
+
+GOOD = 1 << 20  # an aligned address that no accepted call would survive using
+
+
+def _structs():
+    from frame_sparse_attention_b200 import _cache as c
+    rows = c.RowsDesc(2, 4, 2, 8, 64, 1e-6)
+    for t, heads in (("q", 4), ("k", 2), ("v", 2), ("q_out", 4), ("k_out", 2), ("v_out", 2)):
+        for i, s in enumerate((heads * 8 * 64, 8 * 64, 64)):
+            setattr(rows, f"{t}_stride{i}", s)
+    rows.start_stride_b = 1
+    cache = c.CacheDesc(4, 2, 16, 64, GOOD, GOOD, GOOD, GOOD, GOOD, 3, 3, 0)
+    rope = c.RopeDesc(GOOD, GOOD, 8, 1, 0, 1)
+    rope.axis_pairs[0] = 16
+    rope.scale = 1.0
+    return rows, cache, rope
+
+
+def _call(sfa, fn, rows, cache, rope, p=GOOD):
+    lib, r = sfa.load(), ctypes.byref
+    rp = None if rope is None else r(rope)
+    rows = None if rows is None else r(rows)
+    cp = None if cache is None else r(cache)
+    if fn == "norm":
+        return lib.sfa_qk_norm_rope(rows, rp, p, p, None, None, p, p, None)
+    if fn == "write":
+        return lib.sfa_cache_write(rows, cp, p, p, GOOD, None, None, None)
+    if fn == "append":
+        return lib.sfa_cache_append(rows, rp, cp, p, p, p, None, None, p, GOOD, None, None, None)
+    return lib.sfa_cache_read(rows, cp, GOOD, None, p, p, None, None)
+
+
+ALL = ("norm", "write", "append", "read")
+CACHE = ("write", "append", "read")
+
+
+@pytest.mark.parametrize("over,code", [(dict(B=-1), 1), (dict(L=-1), 1), (dict(d=96), 2), (dict(d=32), 2),
+                                       (dict(H_kv=0), 1), (dict(H_kv=2000), 1)])
+@pytest.mark.parametrize("fn", ALL)
+def test_shapes(sfa, fn, over, code):
+    rows, cache, rope = _structs()
+    for k, v in over.items():
+        setattr(rows, k, v)
+    assert _call(sfa, fn, rows, cache, rope) == code
+    assert _call(sfa, fn, None, cache, rope) == 1
+
+
+@pytest.mark.parametrize("over", [dict(eps=float("nan")), dict(eps=float("inf"))])
+@pytest.mark.parametrize("fn", ("norm", "append"))
+def test_eps(sfa, fn, over):
+    rows, cache, rope = _structs()
+    rows.eps = over["eps"]
+    assert _call(sfa, fn, rows, cache, rope) == 1
+
+
+@pytest.mark.parametrize("fn", ALL)
+def test_addresses_and_strides(sfa, fn):
+    rows, cache, rope = _structs()
+    assert _call(sfa, fn, rows, cache, rope, p=GOOD + 2) == 1
+    assert _call(sfa, fn, rows, cache, rope, p=None) == 1
+    for t in {"norm": ("q", "k", "q_out", "k_out"), "write": ("k", "v"), "append": ("q", "k", "v", "q_out"),
+              "read": ("k_out", "v_out")}[fn]:
+        for i, bad in ((0, 0), (1, 12), (2, -64), (2, 1 << 40)):
+            rows, cache, rope = _structs()
+            setattr(rows, f"{t}_stride{i}", bad)
+            assert _call(sfa, fn, rows, cache, rope) == 1, (t, i, bad)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(n_pages=0), 1), (dict(heads=3), 1), (dict(page_len=0), 1), (dict(d=128), 1), (dict(d=48), 2), (dict(k=None), 1),
+    (dict(v_scale=None), 1), (dict(table=None), 1), (dict(k=GOOD + 8), 1), (dict(k_scale=GOOD + 1), 1), (dict(table_len=0), 1),
+    (dict(table_stride_b=-1), 1), (dict(table_len=1 << 20, page_len=1 << 12), 1)])
+@pytest.mark.parametrize("fn", CACHE)
+def test_cache(sfa, fn, over, code):
+    rows, cache, rope = _structs()
+    for k, v in over.items():
+        setattr(cache, k, v)
+    assert _call(sfa, fn, rows, cache, rope) == code
+    assert _call(sfa, fn, rows, None, rope) == 1
+
+
+@pytest.mark.parametrize("fn", CACHE)
+def test_start(sfa, fn):
+    rows, cache, rope = _structs()
+    rows.start_stride_h = -1
+    assert _call(sfa, fn, rows, cache, rope) == 1
+
+
+@pytest.mark.parametrize("over,pairs,code", [
+    (dict(inv_freq=None), (16,), 1), (dict(positions=None), (16,), 1), (dict(inv_freq=GOOD + 4), (16,), 1),
+    (dict(positions=GOOD + 2), (16,), 1), (dict(layout=2), (16,), 1), (dict(n_axes=0), (), 1), (dict(n_axes=5), (), 1),
+    (dict(scale=float("nan")), (16,), 1), (dict(pos_stride_t=-1), (16,), 1), (dict(), (0,), 1), (dict(), (33,), 1),
+    (dict(n_axes=2), (20, 20), 1), (dict(n_axes=2), (-1, 20), 1), (dict(layout=1), (12,), 2)])
+@pytest.mark.parametrize("fn", ("norm", "append"))
+def test_rope(sfa, fn, over, pairs, code):
+    rows, cache, rope = _structs()
+    for k, v in over.items():
+        setattr(rope, k, v)
+    for i, p in enumerate(pairs):
+        rope.axis_pairs[i] = p
+    assert _call(sfa, fn, rows, cache, rope) == code
+
+
+@pytest.mark.parametrize("fn", ALL)
+@pytest.mark.parametrize("dim", ("B", "L"))
+def test_nothing_to_do(sfa, fn, dim):
+    rows, cache, rope = _structs()
+    setattr(rows, dim, 0)
+    assert _call(sfa, fn, rows, cache, rope, p=None) == 0
+
+
+def test_norm_rope_needs_an_input_and_its_output(sfa):
+    lib, (rows, _, _) = sfa.load(), _structs()
+    r = ctypes.byref(rows)
+    assert lib.sfa_qk_norm_rope(r, None, None, None, None, None, None, None, None) == 1
+    assert lib.sfa_qk_norm_rope(r, None, GOOD, None, None, None, None, None, None) == 1
+    assert lib.sfa_qk_norm_rope(r, None, GOOD, None, None, None, GOOD, GOOD, None) == 1
+
+
+def test_binding_refuses_wrong_tensors(sfa):
+    q = torch.zeros(2, 4, 8, 64, dtype=torch.bfloat16)
+    k = torch.zeros(2, 2, 8, 64, dtype=torch.bfloat16)
+    cache = sfa.cache_create(4, 16, 64, heads=2, device="cpu")
+    table, start = torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError):  # not on a GPU
+        sfa.qk_norm_rope(q, k)
+    with pytest.raises(ValueError):
+        sfa.cache_write(cache, k, k, table, start)
+    with pytest.raises(ValueError):
+        sfa.cache_append(cache, q, k, k, table, start)
+    with pytest.raises(ValueError):
+        sfa.cache_read(cache, table, start, 8)
+    bad = [dict(k=k.float()), dict(v=k[:, :1]), dict(table=table.long()), dict(table=table[:1]), dict(start=start[:1]),
+           dict(start=start.long()), dict(lens=start.long()), dict(lens=torch.zeros(3, dtype=torch.int32)),
+           dict(cache=sfa.cache_create(4, 16, 128, heads=2, device="cpu")),
+           dict(cache=cache._replace(k_scale=cache.k_scale[..., :1])), dict(cache=cache._replace(k=k)),
+           dict(k=k.transpose(2, 3))]
+    for over in bad:
+        a = dict(cache=cache, k=k, v=k, table=table, start=start, lens=None)
+        a.update(over)
+        with pytest.raises(ValueError):
+            sfa.cache_write(**a)
+    rope = sfa.rope_table((64,), device="cpu")
+    pos = torch.zeros(2, 8, 1, dtype=torch.int32)
+    for over in (dict(positions=None), dict(positions=pos.long()), dict(positions=pos[:, :7]), dict(layout="other"),
+                 dict(rope=rope._replace(inv_freq=rope.inv_freq.float())), dict(rope=rope._replace(axis_pairs=(16,))),
+                 dict(q_weight=torch.ones(63)), dict(q_weight=torch.ones(64).double()), dict(q_out=k)):
+        a = dict(rope=rope, positions=pos)
+        a.update(over)
+        with pytest.raises(ValueError):
+            sfa.qk_norm_rope(q, k, **a)
+    for args, kw in (((63,), {}), ((), {}), ((2,) * 5, {}), ((64,), dict(scaling="other")), ((64,), dict(factor=0.0)),
+                     ((64,), dict(scaling="yarn", factor=2.0))):
+        with pytest.raises(ValueError):
+            sfa.rope_table(args, device="cpu", **kw)
+    with pytest.raises(ValueError):
+        sfa.cache_create(1, 1, 96, device="cpu")
+    assert math.isclose(sfa.rope_table((8,), device="cpu").inv_freq[1].item(), 0.1)
