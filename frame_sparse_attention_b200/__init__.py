@@ -21,6 +21,8 @@ Python face of libsfa.so (C ABI in include/sfa.h):
 * ``qk_norm_rope`` - RMS norm of every head's query and key row and their rotary positions
 * ``cache_write``, ``cache_append``, ``cache_read`` - new keys and values into the pages of an
                     8-bit cache (append: after qk_norm_rope, in the same pass), and back
+* ``forward_cache`` - attention of new tokens, one or a chunk, over that cache: shared key
+                    heads, uneven lengths, causal or not, O bf16 + LSE fp32
 
 Tensors are PyTorch CUDA tensors; calls run on the current CUDA stream.
 """
@@ -33,10 +35,10 @@ from ._lib import (SET_KINDS, SFA_DEBUG_STALL_GDN_STATE, SFA_DEBUG_STALL_SOFTMAX
                    set_max_count,
                    set_params, split_plan, split_workspace_bytes, version)
 from ._cache import (CACHE_BLOCK, FrameCache, RopeTable, cache_append, cache_create, cache_read, cache_write,
-                     qk_norm_rope, rope_table)
+                     forward_cache, forward_cache_workspace_bytes, qk_norm_rope, rope_table)
 
 __all__ = ["CACHE_BLOCK", "FrameCache", "RopeTable", "cache_append", "cache_create", "cache_read", "cache_write",
-           "qk_norm_rope", "rope_table",
+           "forward_cache", "forward_cache_workspace_bytes", "qk_norm_rope", "rope_table",
            "SET_KINDS", "SFA_DEBUG_STALL_GDN_STATE", "SFA_DEBUG_STALL_SOFTMAX", "SFA_ERR_BAD_SET", "SFA_ERR_CUDA",
            "SFA_ERR_INVALID_ARG", "SFA_ERR_TIMEOUT", "SFA_ERR_UNSUPPORTED", "SFA_OK", "AttnDesc",
            "SetParams", "SfaError", "attn_desc", "build_sets", "error_string", "forward", "forward_blocks",

@@ -42,6 +42,15 @@ class RowsDesc(ctypes.Structure):
                [("start_stride_b", _i64), ("start_stride_h", _i64)]
 
 
+class CacheAttnDesc(ctypes.Structure):
+    """sfa_cache_attn_desc."""
+    _fields_ = [("B", _i32), ("H", _i32), ("H_kv", _i32), ("Lq", _i32), ("d", _i32), ("scale", _f32), ("causal", _i32),
+                ("max_kv", _i32)] + \
+               [(f"{t}_stride{i}", _i64) for t in ("q", "o") for i in range(3)] + \
+               [("len_stride_b", _i64), ("len_stride_h", _i64), ("timeout_us", ctypes.c_uint32),
+                ("debug_flags", ctypes.c_uint32)]
+
+
 class RopeTable(NamedTuple):
     """Rotary frequencies: inv_freq float64 [R/2] on the GPU, the pairs of each position axis
     (they add up to R/2), and the factor that long-context scalings put on rotated values."""
@@ -309,3 +318,64 @@ def cache_read(cache: FrameCache, table, start, L: int, lens=None, k_out=None, v
             (ctypes.byref(desc), ctypes.byref(cd), start.data_ptr(), _lens(lens, device, B), k_out.data_ptr(),
              v_out.data_ptr(), _check_status(dev_status, device)), stream, "sfa_cache_read")
     return k_out, v_out
+
+
+def _attn(q, cache, table, kv_lens, causal, max_kv, scale, out, H_kv, timeout_us=0, debug_flags=0):
+    device = q.device
+    B, H, Lq, d = q.shape
+    if H_kv is None:
+        H_kv = max(cache.k.shape[1], table.shape[1] if table.dim() == 3 else 1,
+                   kv_lens.shape[1] if kv_lens.dim() == 2 else 1)
+    cd = _cache_desc(cache, table, device, B, H_kv, d)
+    desc = CacheAttnDesc(B, H, H_kv, Lq, d, 1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0, max_kv,
+                         *q.stride()[:3], *out.stride()[:3], *_per_head("kv_lens", kv_lens, device, B, H_kv),
+                         timeout_us, debug_flags)
+    return desc, cd
+
+
+def forward_cache_workspace_bytes(q, cache: FrameCache, table, kv_lens, max_kv: int = 0, H_kv: int | None = None) -> int:
+    """Device workspace bytes of forward_cache for these shapes."""
+    desc, cd = _attn(q, cache, table, kv_lens, False, max_kv, None, q, H_kv)
+    out = ctypes.c_size_t(0)
+    _check(load().sfa_forward_cache_workspace(ctypes.byref(desc), ctypes.byref(cd), ctypes.byref(out)),
+           "sfa_forward_cache_workspace")
+    return out.value
+
+
+def forward_cache(q, cache: FrameCache, table, kv_lens, causal: bool = False, q_lens=None, max_kv: int = 0,
+                  scale: float | None = None, out=None, lse=None, workspace=None, H_kv: int | None = None,
+                  dev_status=None, stream=None, timeout_us: int = 0, debug_flags: int = 0):
+    """Attention of new tokens over the cache: (O bf16 like q, LSE fp32 [B, H, Lq]).
+
+    q bf16 [B, H, Lq, d]; kv_lens int32 [B] or [B, H_kv]: logical tokens [0, n) are the keys and
+    values.  q_lens int32 [B]: rows from there on are padding, left as they are.  causal: the
+    rows are the last of the n tokens and see none behind themselves.  max_kv: an upper bound of
+    kv_lens, for the split of the work (0: all that the table can hold).  workspace: a uint8
+    tensor of forward_cache_workspace_bytes (allocated here when not given).  H_kv: key heads,
+    where neither the pool, the table nor kv_lens says so.  Rows that see no key give O = 0,
+    LSE = -inf, so the result merges with other branches by lse_merge."""
+    device = q.device
+    _rows("q", q, device)
+    B, H, Lq, d = q.shape
+    out = torch.empty_like(q) if out is None else out
+    _rows("out", out, device, q.shape)
+    if lse is None:
+        lse = torch.empty((B, H, Lq), dtype=torch.float32, device=device)
+    elif lse.dtype != torch.float32 or lse.device != device or tuple(lse.shape) != (B, H, Lq) or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous fp32 tensor {(B, H, Lq)} on {device}")
+    desc, cd = _attn(q, cache, table, kv_lens, causal, max_kv, scale, out, H_kv, timeout_us, debug_flags)
+    lib = load()
+    if workspace is None:
+        need = ctypes.c_size_t(0)
+        _check(lib.sfa_forward_cache_workspace(ctypes.byref(desc), ctypes.byref(cd), ctypes.byref(need)),
+               "sfa_forward_cache_workspace")
+        if need.value:
+            workspace = torch.empty(need.value, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _launch(device, lib.sfa_forward_cache,
+            (ctypes.byref(desc), ctypes.byref(cd), q.data_ptr(), kv_lens.data_ptr(), _lens(q_lens, device, B),
+             out.data_ptr(), lse.data_ptr(), ws, ws_bytes, _check_status(dev_status, device)), stream,
+            "sfa_forward_cache")
+    return out, lse

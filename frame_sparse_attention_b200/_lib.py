@@ -65,7 +65,8 @@ EXPORTS = ("sfa_error_string", "sfa_version", "sfa_set_max_count", "sfa_build_se
            "sfa_forward_blocks_split", "sfa_forward_blocks_split_workspace", "sfa_forward_split_plan",
            "sfa_forward_host_workspace", "sfa_forward_host", "sfa_hsa_pool_keys", "sfa_hsa_select_pooled",
            "sfa_forward_dual_workspace", "sfa_forward_dual", "sfa_gdn_workspace", "sfa_gdn_forward",
-           "sfa_qk_norm_rope", "sfa_cache_write", "sfa_cache_append", "sfa_cache_read")
+           "sfa_qk_norm_rope", "sfa_cache_write", "sfa_cache_append", "sfa_cache_read",
+           "sfa_forward_cache_workspace", "sfa_forward_cache")
 
 
 def load():
@@ -142,6 +143,10 @@ def load():
         fn = getattr(lib, name)
         fn.restype = st
         fn.argtypes = [vp] * (n + 1)
+    lib.sfa_forward_cache_workspace.restype = st
+    lib.sfa_forward_cache_workspace.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_size_t)]
+    lib.sfa_forward_cache.restype = st
+    lib.sfa_forward_cache.argtypes = [vp] * 8 + [ctypes.c_size_t, vp, vp]
     _lib = lib
     return lib
 

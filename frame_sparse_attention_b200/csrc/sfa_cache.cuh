@@ -49,8 +49,10 @@ inline sfa_status check_cache(const sfa_cache *c, int32_t H_kv, int32_t d)
         reinterpret_cast<uintptr_t>(c->table) % 4)
         return SFA_ERR_INVALID_ARG;
     if (c->table_stride[0] < 0 || c->table_stride[1] < 0) return SFA_ERR_INVALID_ARG;
-    // a logical token is an int32, and so is a table offset times page_len
-    if ((int64_t)c->table_len * c->page_len >= ((int64_t)1 << 31)) return SFA_ERR_INVALID_ARG;
+    // a logical token is an int32 with room for a tile behind it, and a pool row is an int32
+    // (2^31 rows of codes are past any GPU's memory)
+    if ((int64_t)c->table_len * c->page_len >= ((int64_t)1 << 30)) return SFA_ERR_INVALID_ARG;
+    if ((int64_t)c->n_pages * c->heads >= ((int64_t)1 << 31) / c->page_len) return SFA_ERR_INVALID_ARG;
     return SFA_OK;
 }
 

@@ -493,7 +493,7 @@ sfa_status sfa_gdn_forward(const sfa_gdn_desc *desc, const void *q, const void *
 #define SFA_CACHE_BLOCK 32
 
 typedef struct {
-    int32_t n_pages;   /* pages of the pool, >= 1                                          */
+    int32_t n_pages;   /* pages of the pool, >= 1; n_pages * heads * page_len < 2^31        */
     int32_t heads;     /* heads of a page: H_kv (the heads share a page's number), or 1 (a
                           page belongs to one head, so that heads can keep different frames) */
     int32_t page_len;  /* rows of a page, >= 1                                             */
@@ -502,7 +502,7 @@ typedef struct {
     void *k_scale, *v_scale; /* e + 127 as uint8 [n_pages][heads][page_len][d / 32], contiguous,
                                 aligned to d / 32 bytes                                    */
     const int32_t *table;    /* device page numbers, see table_stride                      */
-    int32_t table_len;       /* entries of a table row, >= 1                               */
+    int32_t table_len;       /* entries of a table row, >= 1; table_len * page_len < 2^30   */
     int64_t table_stride[2]; /* batch, key head (in entries; 0: the row is shared)         */
 } sfa_cache;
 
@@ -573,6 +573,45 @@ sfa_status sfa_cache_append(const sfa_rows_desc *desc, const sfa_rope *rope, con
  * SFA_ERR_BAD_SET), are left as they are. */
 sfa_status sfa_cache_read(const sfa_rows_desc *desc, const sfa_cache *cache, const int32_t *start,
                           const int32_t *lens, void *k_out, void *v_out, int32_t *dev_status, sfa_stream_t stream);
+
+/*
+ * Attention of a chunk of new tokens over the cache ("Head Forcing", §2: the chunk attends
+ * each head's own cache; "LVSA", §2: softmax attention with its log-sum-exp).
+ *   q, o      bf16 [B][H][Lq][d], strides in the descriptor; head h reads key head h / (H / H_kv).
+ *   kv_lens   device int32, n = kv_lens[b * len_stride[0] + hk * len_stride[1]]: the keys and
+ *             values are logical tokens [0, n) of (b, hk).  n = 0 gives O = 0, LSE = -inf.
+ *   q_lens    device int32 [B] or NULL (= Lq): only rows i < m = q_lens[b] exist; the others
+ *             of o and lse are left as they are.
+ *   causal    != 0: row i sees tokens j <= n - m + i (the m rows are the last of the n
+ *             tokens); a row that sees none gives O = 0, LSE = -inf.
+ *   lse       fp32 [B][H][Lq], contiguous: ln of the sum of exp(scale q.k) over the row's keys.
+ *   max_kv    an upper bound of the n of this call, by which the keys are cut into ranges
+ *             that run side by side (0: table_len * page_len).  It sets the speed, never the
+ *             result's meaning: longer caches are attended in full all the same.
+ *   workspace device memory of sfa_forward_cache_workspace bytes, 256-byte aligned, scratch
+ *             (NULL where that is 0).  Calls that can overlap need one each.
+ * Keys at and behind n, and other pages, may hold anything.  An n outside
+ * [0, table_len * page_len] or a page number outside the pool is reported as
+ * SFA_ERR_BAD_SET in dev_status; the rows of that (b, hk) are then unspecified, and nothing
+ * outside the pool is read.  Scores, softmax and partial results are fp32; the
+ * probabilities are rounded to bf16 for the product with V, as in sfa_forward.
+ */
+typedef struct {
+    int32_t B, H, H_kv, Lq, d;
+    float scale;               /* > 0, finite                                              */
+    int32_t causal;
+    int32_t max_kv;
+    int64_t q_stride[3], o_stride[3]; /* batch, head, token                                */
+    int64_t len_stride[2];     /* of kv_lens: batch, key head (0: shared)                  */
+    uint32_t timeout_us;       /* limit of every pipeline wait in the kernel; 0 = 2 s      */
+    uint32_t debug_flags;      /* SFA_DEBUG_* ; 0 in normal use                            */
+} sfa_cache_attn_desc;
+
+sfa_status sfa_forward_cache_workspace(const sfa_cache_attn_desc *desc, const sfa_cache *cache, size_t *bytes);
+
+sfa_status sfa_forward_cache(const sfa_cache_attn_desc *desc, const sfa_cache *cache, const void *q,
+                             const int32_t *kv_lens, const int32_t *q_lens, void *o, float *lse, void *workspace,
+                             size_t workspace_bytes, int32_t *dev_status, sfa_stream_t stream);
 
 /* ------------------------------------------------------------------------------------
  * LSE merge

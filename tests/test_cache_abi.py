@@ -175,3 +175,70 @@ def test_binding_refuses_wrong_tensors(sfa):
     with pytest.raises(ValueError):
         sfa.cache_create(1, 1, 96, device="cpu")
     assert math.isclose(sfa.rope_table((8,), device="cpu").inv_freq[1].item(), 0.1)
+
+
+def _attn(sfa):
+    from frame_sparse_attention_b200 import _cache as c
+    d = c.CacheAttnDesc(2, 4, 2, 8, 64, 0.125, 0, 0)
+    for t in ("q", "o"):
+        for i, s in enumerate((4 * 8 * 64, 8 * 64, 64)):
+            setattr(d, f"{t}_stride{i}", s)
+    d.len_stride_b = 1
+    return d
+
+
+def _attn_call(sfa, d, cache, q=GOOD, o=GOOD, lse=GOOD, lens=GOOD, ws=None, ws_bytes=0):
+    r = ctypes.byref
+    return sfa.load().sfa_forward_cache(None if d is None else r(d), None if cache is None else r(cache), q, lens, None, o,
+                                        lse, ws, ws_bytes, None, None)
+
+
+@pytest.mark.parametrize("over,code", [(dict(B=-1), 1), (dict(Lq=-1), 1), (dict(d=96), 2), (dict(H=0), 1), (dict(H=3), 1),
+                                       (dict(H_kv=0), 1), (dict(H_kv=4), 1), (dict(scale=0.0), 1), (dict(scale=-1.0), 1),
+                                       (dict(scale=float("inf")), 1), (dict(max_kv=-1), 1), (dict(len_stride_b=-1), 1),
+                                       (dict(q_stride1=12), 1), (dict(o_stride2=0), 1), (dict(d=128), 1)])
+def test_attention_descriptor(sfa, over, code):
+    _, cache, _ = _structs()
+    d = _attn(sfa)
+    for k, v in over.items():
+        setattr(d, k, v)
+    assert _attn_call(sfa, d, cache) == code
+
+
+def test_attention_addresses(sfa):
+    _, cache, _ = _structs()
+    d = _attn(sfa)
+    assert _attn_call(sfa, None, cache) == 1 and _attn_call(sfa, d, None) == 1
+    for k in ("q", "o", "lse", "lens"):
+        assert _attn_call(sfa, d, cache, **{k: None}) == 1
+    assert _attn_call(sfa, d, cache, q=GOOD + 8) == 1 and _attn_call(sfa, d, cache, o=GOOD + 2) == 1
+    d.Lq = 0
+    assert _attn_call(sfa, d, cache, q=None) == 0
+
+
+def test_attention_workspace(sfa):
+    _, cache, _ = _structs()
+    d = _attn(sfa)
+    cache.table_len, cache.page_len = 4096, 16  # 65536 tokens: the keys are cut into ranges
+    need = ctypes.c_size_t(0)
+    lib, r = sfa.load(), ctypes.byref
+    assert lib.sfa_forward_cache_workspace(r(d), r(cache), r(need)) == 0 and need.value > 0 and need.value % 256 == 0
+    assert _attn_call(sfa, d, cache) == 1                                           # none
+    assert _attn_call(sfa, d, cache, ws=GOOD, ws_bytes=need.value - 1) == 1         # too small
+    assert _attn_call(sfa, d, cache, ws=GOOD + 128, ws_bytes=need.value) == 1       # misaligned
+    d.max_kv = 100
+    assert lib.sfa_forward_cache_workspace(r(d), r(cache), r(need)) == 0 and need.value == 0
+    assert lib.sfa_forward_cache_workspace(r(d), r(cache), None) == 1
+
+
+def test_attention_binding_refuses_wrong_tensors(sfa):
+    q = torch.zeros(2, 4, 8, 64, dtype=torch.bfloat16)
+    cache = sfa.cache_create(4, 16, 64, heads=2, device="cpu")
+    table, lens = torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for over in (dict(), dict(q=q.float()), dict(kv_lens=lens.long()), dict(kv_lens=lens[:1]), dict(table=table.long()),
+                 dict(out=q[:1]), dict(lse=torch.zeros(2, 4, 7)), dict(lse=torch.zeros(2, 4, 8).double()),
+                 dict(q_lens=lens.long()), dict(H_kv=3), dict(q=q[..., :32]), dict(cache=cache._replace(v=cache.v[:2]))):
+        a = dict(q=q, cache=cache, table=table, kv_lens=lens)
+        a.update(over)
+        with pytest.raises((ValueError, sfa.SfaError)):
+            sfa.forward_cache(**a)
