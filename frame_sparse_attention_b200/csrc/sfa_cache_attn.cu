@@ -13,12 +13,14 @@
 // the loads of the next keys are issued as soon as the registers are free; the key range is
 // cut over warps and CTAs so that all SMs stream, and the partial results are joined by their
 // log-sum-exp.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
 #include <cuda_runtime.h>
 
 #include "sfa.h"
+#include "sfa_attn_core.cuh"
 #include "sfa_cache.cuh"
 #include "sfa_internal.h"
 #include "sfa_ptx.cuh"
@@ -39,6 +41,7 @@ struct ChunkArgs {
     float *lse;
     int32_t *status;
     int32_t n_row_tiles, n_split;
+    int32_t range_len;  // key steps of a range, see n_ranges
     float *part_o;    // [n_split][B * H * Lq][d], normalised, when n_split > 1
     float *part_lse;  // [n_split][B * H * Lq], log2 units
     uint64_t timeout_ns;
@@ -60,7 +63,9 @@ __device__ __forceinline__ Unit open_unit(const ChunkArgs &a, int tile_rows)
     int x = blockIdx.x;
     u.split = x % a.n_split;
     x /= a.n_split;
-    u.row0 = (x % a.n_row_tiles) * tile_rows;
+    // causal: the last row tiles see the most keys and start first
+    const int rt = x % a.n_row_tiles;
+    u.row0 = (a.causal ? a.n_row_tiles - 1 - rt : rt) * tile_rows;
     x /= a.n_row_tiles;
     u.hk = x % a.Hk;
     u.b = x / a.Hk;
@@ -77,6 +82,28 @@ __device__ __forceinline__ int row_limit(const ChunkArgs &a, const Unit &u, int 
 {
     if (r >= u.n_rows) return 0;
     return a.causal ? max(0, min(u.n, u.n - u.m + r / a.G + 1)) : u.n;
+}
+
+// Ranges that the key steps of a unit are cut into: as many of range_len steps as it has, so
+// that long and short caches give pieces of one length, but no more than the n_split CTAs
+// that it was given (caches longer than the caller's bound just get longer ranges).
+__device__ __forceinline__ int n_ranges(const ChunkArgs &a, int steps)
+{
+    return max(1, min(a.n_split, (steps + a.range_len - 1) / a.range_len));
+}
+
+// Row `id` of the outputs: (b * H + h) * Lq + i for row r of a unit.
+__device__ __forceinline__ int64_t row_id(const ChunkArgs &a, const Unit &u, int r)
+{
+    return ((int64_t)u.b * a.H + u.hk * a.G + r % a.G) * a.Lq + r / a.G;
+}
+
+// A CTA without a range of its own leaves "nothing seen" for its rows.
+__device__ __forceinline__ void skip_range(const ChunkArgs &a, const Unit &u, int tile_rows)
+{
+    const int64_t part_rows = (int64_t)a.B * a.H * a.Lq;
+    for (int r = u.row0 + threadIdx.x; r < min(u.row0 + tile_rows, u.n_rows); r += blockDim.x)
+        a.part_lse[(int64_t)u.split * part_rows + row_id(a, u, r)] = -INFINITY;
 }
 
 // ----------------------------------------------------------------- few query rows
@@ -138,6 +165,11 @@ __global__ void __launch_bounds__(FR_WARPS * 32, 4) rows_attn_kernel(const __gri
     const Unit u = open_unit(a, FR_ROWS);
     if (u.bad && tid == 0) report_status(a.status, SFA_ERR_BAD_SET);
     if (u.row0 >= u.n_rows) return;  // rows behind this sequence's last
+    // the tile's last row sees the most keys
+    const int seen = row_limit(a, u, min(u.row0 + FR_ROWS, u.n_rows) - 1);
+    const int steps = (seen + FR_KEYS - 1) / FR_KEYS;
+    const int ranges = n_ranges(a, steps);
+    if (u.split >= ranges) return skip_range(a, u, FR_ROWS);
 
     // Q in the A-operand layout of every k-step: rows g and g + 8, elements
     // c * 64 + 16 t + 4 w + {0, 1} and {2, 3} of k-step 4 c + w
@@ -157,10 +189,7 @@ __global__ void __launch_bounds__(FR_WARPS * 32, 4) rows_attn_kernel(const __gri
     __syncthreads();
 
     const int lim0 = row_limit(a, u, u.row0 + g), lim1 = row_limit(a, u, u.row0 + g + 8);
-    // the tile's last row sees the most keys
-    const int seen = row_limit(a, u, min(u.row0 + FR_ROWS, u.n_rows) - 1);
-    const int steps = (seen + FR_KEYS - 1) / FR_KEYS;
-    const int s0 = (int)((int64_t)steps * u.split / a.n_split), s1 = (int)((int64_t)steps * (u.split + 1) / a.n_split);
+    const int s0 = (int)((int64_t)steps * u.split / ranges), s1 = (int)((int64_t)steps * (u.split + 1) / ranges);
 
     float o[NT][4];
 #pragma unroll
@@ -366,7 +395,7 @@ __global__ void __launch_bounds__(FR_WARPS * 32, 4) rows_attn_kernel(const __gri
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const float lse2 = l > 0.f ? M + log2f(l) : -INFINITY;
         const int h = u.hk * a.G + row % a.G, i = row / a.G;
-        const int64_t id = ((int64_t)u.b * a.H + h) * a.Lq + i;
+        const int64_t id = row_id(a, u, row);
         if (a.n_split == 1) {
             uint4 v;
             v.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
@@ -381,6 +410,485 @@ __global__ void __launch_bounds__(FR_WARPS * 32, 4) rows_attn_kernel(const __gri
             dst[1] = make_float4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv);
             if (e0 == 0) a.part_lse[(int64_t)u.split * part_rows + id] = lse2;
         }
+    }
+}
+
+// ----------------------------------------------------------------- many query rows
+// Units of two 128-row query tiles against 128-key tiles, on the tensor cores through tensor
+// memory, in the schedule of the frame-list forward kernel (S one tile ahead of the softmax,
+// P V behind it; a unit with one query tile runs S two key tiles ahead).  What differs is how
+// the operands arrive: four warps load the codes of a K and a V tile into registers, a tile
+// ahead, look up their pages, and store them as bf16 in the 128-byte-swizzled layout that
+// the matrix instruction reads, zeros behind the last key; the softmax warps bring their own
+// query rows, since a unit's rows may be those of several heads.
+constexpr int CT_SOFTMAX_WARPS = 8;       // warps 0-3: query tile A, 4-7: B
+constexpr int CT_CONV_WARP = 8;           // 8-11: codes to bf16
+constexpr int CT_CONV_WARPS = 4;
+constexpr int CT_MMA_WARP = 12;
+constexpr int CT_THREADS = 32 * (CT_MMA_WARP + 1);
+constexpr int CT_ROWS = 2 * BM;
+
+// byte offset of the 16-byte piece `ch` (8 elements) of row r in a swizzled tile
+template <int D>
+__device__ __forceinline__ uint32_t swz(int r, int ch)
+{
+    return (uint32_t)((ch >> 3) * Cfg<D>::BOX_BYTES + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+}
+
+// The K and V tiles of the unit, codes to bf16.  Warp w takes rows 32 w .. 32 w + 31 of every
+// tile: lane l looks up row l's place, D/16 lanes then share a row, 16 codes each.
+template <int D>
+__device__ void convert_role(const ChunkArgs &a, const Unit &u, uint32_t sbase, int key0, int key_end, int n_tiles,
+                             const Ctl &ctl)
+{
+    using C = Cfg<D>;
+    constexpr int LR = D / 16;        // lanes per row
+    constexpr int RPI = 32 / LR;      // rows per load of the warp
+    constexpr int NI = 32 / RPI;      // loads per tile
+    typedef typename ScaleWord<D>::type scale_t;
+    const Bars<D> bar{sbase + C::SMEM_BAR};
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - CT_CONV_WARP;
+    const int sub = lane / LR, c = lane % LR;
+
+    auto rows_of = [&](int j) -> int {  // pool row of key 32 w + lane of tile j
+        const int key = key0 + j * BN + w * 32 + lane;
+        if (j >= n_tiles || key >= key_end) return -1;
+        const int64_t r = cache_row(a.cache, u.b, u.hk, key);
+        if (r < 0) report_status(a.status, SFA_ERR_BAD_SET);
+        return (int)r;
+    };
+    auto load = [&](const uint8_t *codes, const uint8_t *scales, int rows, uint4 (&x)[NI], uint32_t &sw) {
+        sw = rows >= 0 ? (uint32_t)__ldg(reinterpret_cast<const scale_t *>(scales) + rows) : 0u;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int r = __shfl_sync(0xffffffffu, rows, i * RPI + sub);
+            x[i] = r >= 0 ? __ldg(reinterpret_cast<const uint4 *>(codes + (int64_t)r * D + c * 16))
+                          : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    auto store = [&](uint32_t tile, const uint4 (&x)[NI], uint32_t sw) {
+        const bool two = __any_sync(0xffffffffu, __vcmpgtu4(sw, 0x01010101u * SCALE_ONE_STEP) != 0u);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int r = i * RPI + sub;  // row inside this warp's 32
+            const uint32_t byte = (__shfl_sync(0xffffffffu, sw, r) >> (8 * (c / 2))) & 0xffu;
+            const uint32_t f = scale_bits(byte) * 0x10001u;
+            const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t y[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                y[2 * k] = codes_in_word<0>(in[k], f);
+                y[2 * k + 1] = codes_in_word<2>(in[k], f);
+            }
+            if (two) {
+                const uint32_t g = scale_rest_bits(byte) * 0x10001u;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = mul_bf16x2(y[k], g);
+            }
+            const uint32_t lo[4] = {y[0], y[1], y[2], y[3]}, hi[4] = {y[4], y[5], y[6], y[7]};
+            // the upper half of a row's lanes store their two pieces in the other order, so that
+            // the eight lanes of one access fall on all eight 16-byte bank groups
+            const bool swap = D == 128 && c >= 4;
+            const int row = w * 32 + r;
+            st_shared_v4(tile + swz<D>(row, 2 * c + (swap ? 1 : 0)), swap ? hi : lo);
+            st_shared_v4(tile + swz<D>(row, 2 * c + (swap ? 0 : 1)), swap ? lo : hi);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+    };
+
+    uint4 kx[NI], vx[NI];
+    uint32_t ks, vs;
+    int rows_k = rows_of(0), rows_v;
+    load(a.cache.k, a.cache.k_scale, rows_k, kx, ks);
+    load(a.cache.v, a.cache.v_scale, rows_k, vx, vs);
+    // K(0) | K(j + 1) V(j) | ...
+    for (int j = -1; j < n_tiles; ++j) {
+        if (j + 1 < n_tiles) {
+            const int s = (j + 1) % C::NSK, use = (j + 1) / C::NSK;
+            if (use > 0 && !__all_sync(0xffffffffu, wait_bar(bar.k_free(s), (use - 1) & 1, ctl))) return;
+            store(sbase + C::SMEM_K + s * C::TILE_BYTES, kx, ks);
+            if (lane == 0) mbar_arrive(bar.k_full(s));
+            rows_v = rows_k;  // of tile j + 1, for its V
+            rows_k = rows_of(j + 2);
+            load(a.cache.k, a.cache.k_scale, rows_k, kx, ks);
+        } else {
+            rows_v = -1;
+        }
+        if (j >= 0) {
+            const int s = j % C::NSV, use = j / C::NSV;
+            if (use > 0 && !__all_sync(0xffffffffu, wait_bar(bar.v_free(s), (use - 1) & 1, ctl))) return;
+            store(sbase + C::SMEM_V + s * C::TILE_BYTES, vx, vs);
+            if (lane == 0) mbar_arrive(bar.v_full(s));
+            load(a.cache.v, a.cache.v_scale, rows_v, vx, vs);
+        }
+    }
+}
+
+template <int D>
+__device__ void chunk_mma_pair(uint32_t sbase, uint32_t tmem, int n_tiles, const Ctl &ctl)
+{
+    using C = Cfg<D>;
+    constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, false);
+    const Bars<D> bar{sbase + C::SMEM_BAR};
+    const uint64_t dq = sdesc_sw128(sbase + C::SMEM_Q, 16, 1024), dk = sdesc_sw128(sbase + C::SMEM_K, 16, 1024);
+    const uint64_t dv = sdesc_sw128(sbase + C::SMEM_V, C::BOX_BYTES, 1024), dp = sdesc_sw128(sbase + C::SMEM_P, 16, 1024);
+    bool issued = false;
+    if (!__all_sync(0xffffffffu, wait_bar(bar.q_full(), 0, ctl))) goto done;
+    if (!__all_sync(0xffffffffu, wait_bar(bar.k_full(0), 0, ctl))) goto done;
+    tc_fence_after();
+    for (int x = 0; x < 2; ++x) {
+        issue_s<D>(tmem + tcol_s(x), desc_add(dq, x * C::TILE_BYTES), dk, idesc_s);
+        commit_one(bar.s_full(x));
+    }
+    commit_one(bar.k_free(0));
+    issued = true;
+    for (int j = 0; j < n_tiles; ++j) {
+        const int sv = j % C::NSV, sk = (j + 1) % C::NSK;
+        for (int x = 0; x < 2; ++x) {
+            if (!__all_sync(0xffffffffu, wait_bar(bar.p_full(x), j & 1, ctl))) goto done;
+            if (j + 1 < n_tiles) {
+                if (x == 0 && !__all_sync(0xffffffffu, wait_bar(bar.k_full(sk), ((j + 1) / C::NSK) & 1, ctl))) goto done;
+                tc_fence_after();
+                issue_s<D>(tmem + tcol_s(x), desc_add(dq, x * C::TILE_BYTES), desc_add(dk, sk * C::TILE_BYTES), idesc_s);
+                commit_one(bar.s_full(x));
+                if (x == 1) commit_one(bar.k_free(sk));
+            }
+            if (x == 0 && !__all_sync(0xffffffffu, wait_bar(bar.v_full(sv), (j / C::NSV) & 1, ctl))) goto done;
+            tc_fence_after();
+            issue_pv<D>(tmem + tcol_o(x), desc_add(dp, x * C::P_BYTES), desc_add(dv, sv * C::TILE_BYTES), BN, j > 0);
+            commit_one(bar.pv_x(x));
+            if (x == 1) {
+                commit_one(bar.v_free(sv));
+                if (j == n_tiles - 1) commit_one(bar.o_final());
+            }
+        }
+    }
+done:
+    if (__any_sync(0xffffffffu, *ctl.abort != 0) && issued) {  // the tensor cores finish before TMEM is released
+        commit_one(bar.drain());
+        wait_drain(bar.drain(), 0);
+    }
+    __syncwarp();
+}
+
+template <int D>
+__device__ void chunk_mma_single(uint32_t sbase, uint32_t tmem, int n_tiles, const Ctl &ctl)
+{
+    using C = Cfg<D>;
+    constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, false);
+    const Bars<D> bar{sbase + C::SMEM_BAR};
+    const uint64_t dq = sdesc_sw128(sbase + C::SMEM_Q, 16, 1024), dk = sdesc_sw128(sbase + C::SMEM_K, 16, 1024);
+    const uint64_t dv = sdesc_sw128(sbase + C::SMEM_V, C::BOX_BYTES, 1024), dp = sdesc_sw128(sbase + C::SMEM_P, 16, 1024);
+    bool issued = false;
+    if (!__all_sync(0xffffffffu, wait_bar(bar.q_full(), 0, ctl))) goto done;
+    for (int j = 0; j < 2 && j < n_tiles; ++j) {
+        const int sk = j % C::NSK;
+        if (!__all_sync(0xffffffffu, wait_bar(bar.k_full(sk), (j / C::NSK) & 1, ctl))) goto done;
+        tc_fence_after();
+        issue_s<D>(tmem + tcol_s(j), dq, desc_add(dk, sk * C::TILE_BYTES), idesc_s);
+        commit_one(bar.s_full(j));
+        commit_one(bar.k_free(sk));
+        issued = true;
+    }
+    for (int j = 0; j < n_tiles; ++j) {
+        const int bj = j & 1, sv = j % C::NSV;
+        if (!__all_sync(0xffffffffu, wait_bar(bar.p_full(bj), (j >> 1) & 1, ctl))) goto done;
+        if (!__all_sync(0xffffffffu, wait_bar(bar.v_full(sv), (j / C::NSV) & 1, ctl))) goto done;
+        tc_fence_after();
+        issue_pv<D>(tmem + tcol_o(0), desc_add(dp, bj * C::P_BYTES), desc_add(dv, sv * C::TILE_BYTES), BN, j > 0);
+        commit_one(bar.pv_done());
+        commit_one(bar.v_free(sv));
+        if (j == n_tiles - 1) commit_one(bar.o_final());
+        if (j + 2 < n_tiles) {
+            const int sk = (j + 2) % C::NSK;
+            if (!__all_sync(0xffffffffu, wait_bar(bar.k_full(sk), ((j + 2) / C::NSK) & 1, ctl))) goto done;
+            tc_fence_after();
+            issue_s<D>(tmem + tcol_s(bj), dq, desc_add(dk, sk * C::TILE_BYTES), idesc_s);
+            commit_one(bar.s_full(bj));
+            commit_one(bar.k_free(sk));
+        }
+    }
+done:
+    if (__any_sync(0xffffffffu, *ctl.abort != 0) && issued) {
+        commit_one(bar.drain());
+        wait_drain(bar.drain(), 0);
+    }
+    __syncwarp();
+}
+
+template <bool MASK>
+__device__ __forceinline__ void hide_columns(int c, int nv, uint32_t (&r)[32])
+{
+    if (MASK && c * 32 + 32 > nv) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (c * 32 + i >= nv) r[i] = __float_as_uint(-INFINITY);
+    }
+}
+
+// One key tile of the online softmax, as softmax_tile of the frame-list kernel, for rows that
+// see columns [0, nv) of the tile each (MASK; all of them otherwise).  m_used stays -inf, and
+// the row's probabilities 0, until the row has seen a key.
+template <int D, bool MASK>
+__device__ __forceinline__ bool chunk_softmax_tile(uint32_t t_s, uint32_t p_row, int row, uint32_t t_o, int nv, float sl2,
+                                                   float &m_used, float &l, int j, uint32_t pv_done, uint32_t pv_first,
+                                                   const Ctl &ctl)
+{
+    if (j > 0) {  // streaming pass against the current max
+        Acc8 acc;
+        const float neg_m = MASK && m_used == -INFINITY ? 0.f : -m_used;
+        uint32_t ra[32], rb[32];
+        tmem_ld32(t_s, ra);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t(&cur)[32] = (c & 1) ? rb : ra;
+            uint32_t(&nxt)[32] = (c & 1) ? ra : rb;
+            tmem_wait_ld_regs(cur);
+            if (c + 1 < 4) tmem_ld32(t_s + (c + 1) * 32, nxt);
+            hide_columns<MASK>(c, nv, cur);
+            if (c == 0 && pv_first) {
+                uint32_t pk[16];
+                exp_chunk(cur, sl2, neg_m, pk, acc);
+                if (!__all_sync(0xffffffffu, wait_bar(pv_first, (j - 1) & 1, ctl))) return false;
+                tc_fence_after();
+                store_chunk(pk, p_row, row, 0);
+            } else {
+                exp_store_chunk(cur, sl2, neg_m, p_row, row, c, acc);
+            }
+        }
+        const float lt = sum8(acc);
+        if (!__any_sync(0xffffffffu, lt > RESCALE_LIMIT || m_used == -INFINITY)) {
+            l += lt;
+            return true;
+        }
+    }
+    float mx = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t r[32];
+        tmem_ld32(t_s + c * 32, r);
+        tmem_wait_ld_regs(r);
+        hide_columns<MASK>(c, nv, r);
+        mx = fmaxf(mx, max32(r));
+    }
+    const float m_cand = mx * sl2;
+    const bool resc = m_cand > m_used;
+    const float m_new = resc ? m_cand : m_used;
+    const float neg_m = m_new == -INFINITY ? 0.f : -m_new;
+    const float alpha = m_used == -INFINITY ? 0.f : ex2_approx(m_used - m_new);
+    Acc8 acc;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t r[32];
+        tmem_ld32(t_s + c * 32, r);
+        tmem_wait_ld_regs(r);
+        hide_columns<MASK>(c, nv, r);
+        exp_store_chunk(r, sl2, neg_m, p_row, row, c, acc);
+    }
+    if (j > 0 && __any_sync(0xffffffffu, resc)) {
+        if (pv_done) {
+            if (!__all_sync(0xffffffffu, wait_bar(pv_done, (j - 1) & 1, ctl))) return false;
+            tc_fence_after();
+        }
+        const float by = resc ? alpha : 1.f;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(t_o + c * 32, o);
+            tmem_wait_ld_regs(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+            tmem_st32(t_o + c * 32, o);
+        }
+    }
+    l = l * (resc ? alpha : 1.f) + sum8(acc);
+    m_used = m_new;
+    return true;
+}
+
+// Queries, softmax and epilogue of query tile x, one thread per row.
+template <int D>
+__device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *smem, uint32_t sbase, uint32_t tmem, int x,
+                                   int key0, int n_tiles, bool one_tile, const Ctl &ctl)
+{
+    using C = Cfg<D>;
+    constexpr int LR = D / 8;     // lanes per 16-byte-pieced row
+    constexpr int RPI = 32 / LR;  // rows per access of a warp
+    const Bars<D> bar{sbase + C::SMEM_BAR};
+    volatile int32_t *epi_ok = reinterpret_cast<volatile int32_t *>(smem + C::SMEM_BAR + 160) + 4 * x;
+    const int row = threadIdx.x & 127, lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+    const int tile_row0 = u.row0 + x * BM;
+    const uint32_t s_tile = sbase + C::SMEM_Q + x * C::TILE_BYTES;
+    // this warp's 32 query rows, whole rows at a time
+#pragma unroll 8
+    for (int i = 0; i < 32; i += RPI) {
+        const int rr = warp * 32 + i + lane / LR, ch = lane % LR, r = tile_row0 + rr;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (r < u.n_rows)
+            v = *reinterpret_cast<const uint4 *>(a.q + u.b * a.qs[0] + (u.hk * a.G + r % a.G) * a.qs[1] +
+                                                 (r / a.G) * a.qs[2] + ch * 8);
+        const uint32_t y[4] = {v.x, v.y, v.z, v.w};
+        st_shared_v4(s_tile + swz<D>(rr, ch), y);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar.q_full());
+
+    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t t_o = lane_base + tcol_o(x);
+    const int r = tile_row0 + row;
+    // keys this row sees, from the range's first on; rows that are not there see all (of zeros)
+    const int lim = r < u.n_rows ? row_limit(a, u, r) - key0 : 0x7fffffff;
+    // rows grow in what they see, so a tile that the warp's first row sees whole needs no mask
+    const int lim_warp = __reduce_min_sync(0xffffffffu, lim);
+    float m_used = -INFINITY, l = 0.f;
+    bool alive = true;
+    for (int j = 0; j < n_tiles; ++j) {
+        const int xb = one_tile ? (j & 1) : x;
+        const uint32_t par = one_tile ? (uint32_t)(j >> 1) & 1 : (uint32_t)j & 1;
+        const uint32_t t_s = lane_base + tcol_s(xb);
+        const uint32_t p_row = sbase + C::SMEM_P + xb * C::P_BYTES + row * 128;
+        if (!__all_sync(0xffffffffu, wait_bar(bar.s_full(xb), par, ctl))) {
+            alive = false;
+            break;
+        }
+        tc_fence_after();
+        const uint32_t pvw = one_tile ? bar.pv_done() : 0u;
+        const uint32_t pvf = (!one_tile && j > 0) ? bar.pv_x(x) : 0u;
+        const bool whole = lim_warp >= (j + 1) * BN;
+        const bool ok = whole ? chunk_softmax_tile<D, false>(t_s, p_row, row, t_o, BN, a.scale_log2, m_used, l, j, pvw, pvf, ctl)
+                              : chunk_softmax_tile<D, true>(t_s, p_row, row, t_o, lim - j * BN, a.scale_log2, m_used, l, j,
+                                                            pvw, pvf, ctl);
+        if (!ok) {
+            alive = false;
+            break;
+        }
+        tmem_wait_st();
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && !((a.debug_flags & SFA_DEBUG_STALL_SOFTMAX) && j == 0)) mbar_arrive(bar.p_full(xb));
+    }
+
+    bool have = alive;
+    if (have && n_tiles > 0) have = __all_sync(0xffffffffu, wait_bar(bar.o_final(), 0, ctl));
+    if (lane == 0) epi_ok[warp] = have ? 1 : 0;
+    named_bar_sync(1 + x, BM);
+    if (!(epi_ok[0] && epi_ok[1] && epi_ok[2] && epi_ok[3])) return;  // uniform over the tile's warps
+    const float inv_l = l > 0.f ? 1.f / l : 0.f;
+    const float lse2 = l > 0.f ? m_used + log2f(l) : -INFINITY;
+    const bool there = r < u.n_rows;
+    const int64_t part_rows = (int64_t)a.B * a.H * a.Lq;
+    if (n_tiles > 0) tc_fence_after();
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (n_tiles > 0) {
+            tmem_ld32(t_o + c * 32, o);
+            tmem_wait_ld_regs(o);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
+        }
+        if (a.n_split > 1) {
+            if (there) {
+                float4 *dst = reinterpret_cast<float4 *>(a.part_o + (u.split * part_rows + row_id(a, u, r)) * D + c * 32);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    dst[q] = make_float4(__uint_as_float(o[4 * q]) * inv_l, __uint_as_float(o[4 * q + 1]) * inv_l,
+                                         __uint_as_float(o[4 * q + 2]) * inv_l, __uint_as_float(o[4 * q + 3]) * inv_l);
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    y[i] = pack_bf16x2(__uint_as_float(o[q * 8 + 2 * i]) * inv_l, __uint_as_float(o[q * 8 + 2 * i + 1]) * inv_l);
+                st_shared_v4(s_tile + swz<D>(row, c * 4 + q), y);
+            }
+        }
+    }
+    if (there) {
+        if (a.n_split > 1) a.part_lse[u.split * part_rows + row_id(a, u, r)] = lse2;
+        else a.lse[row_id(a, u, r)] = lse2 * 0.69314718055994530942f;
+    }
+    if (a.n_split > 1) return;
+    __syncwarp();  // a warp stores the 32 rows that its lanes have staged
+#pragma unroll 4
+    for (int i = 0; i < 32; i += RPI) {
+        const int rr = warp * 32 + i + lane / LR, ch = lane % LR, ro = tile_row0 + rr;
+        if (ro < u.n_rows)
+            *reinterpret_cast<uint4 *>(a.o + u.b * a.os[0] + (u.hk * a.G + ro % a.G) * a.os[1] + (ro / a.G) * a.os[2] +
+                                       ch * 8) = *reinterpret_cast<const uint4 *>(smem + (s_tile - sbase) + swz<D>(rr, ch));
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(CT_THREADS, 1) tile_attn_kernel(const __grid_constant__ ChunkArgs a)
+{
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::SMEM_BAR + 240);
+    volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(smem + C::SMEM_BAR + 244);
+    volatile int32_t *skip = reinterpret_cast<volatile int32_t *>(smem + C::SMEM_BAR + 248);
+    const int warp = threadIdx.x >> 5;
+    if (a.n_split > 1) pdl_launch_dependents();
+    const Unit u = open_unit(a, CT_ROWS);
+    if (u.bad && threadIdx.x == 0) report_status(a.status, SFA_ERR_BAD_SET);
+    if (u.row0 >= u.n_rows) return;
+    const int seen = row_limit(a, u, min(u.row0 + CT_ROWS, u.n_rows) - 1);
+    const int all = (seen + BN - 1) / BN;
+    const int ranges = n_ranges(a, all);
+    if (u.split >= ranges) return skip_range(a, u, CT_ROWS);
+    const int t0 = (int)((int64_t)all * u.split / ranges);
+    int n_tiles = (int)((int64_t)all * (u.split + 1) / ranges) - t0;
+    const bool has_b = u.row0 + BM < u.n_rows;
+
+    if (threadIdx.x == 0) {
+        const Bars<D> bar{sbase + C::SMEM_BAR};
+        for (int i = 0; i < Bars<D>::COUNT; ++i) mbar_init(sbase + C::SMEM_BAR + 8 * i, 1);
+        for (int s = 0; s < C::NSK; ++s) mbar_init(bar.k_full(s), CT_CONV_WARPS);
+        for (int s = 0; s < C::NSV; ++s) mbar_init(bar.v_full(s), CT_CONV_WARPS);
+        mbar_init(bar.q_full(), has_b ? CT_SOFTMAX_WARPS : CT_SOFTMAX_WARPS / 2);
+        mbar_init(bar.p_full(0), BM / 32);
+        mbar_init(bar.p_full(1), BM / 32);
+        *abort_flag = 0;
+        // once a CTA has timed out, the ones that start later skip their work
+        *skip = (a.status && *reinterpret_cast<volatile int32_t *>(a.status) == SFA_ERR_TIMEOUT) ? 1 : 0;
+        fence_mbar_init();
+    }
+    if (warp == CT_MMA_WARP) {
+        tmem_alloc(smem_u32(tmem_slot), TM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const Ctl ctl{abort_flag, a.status, a.timeout_ns};
+    const bool skipped = *skip != 0;
+    if (skipped) n_tiles = 0;
+
+    if (warp == CT_MMA_WARP) {
+        if (n_tiles > 0) {
+            if (has_b) chunk_mma_pair<D>(sbase, tmem, n_tiles, ctl);
+            else chunk_mma_single<D>(sbase, tmem, n_tiles, ctl);
+        }
+    } else if (warp >= CT_CONV_WARP) {
+        if (n_tiles > 0) convert_role<D>(a, u, sbase, t0 * BN, seen, n_tiles, ctl);
+    } else if (!skipped && (warp < 4 || has_b)) {
+        chunk_softmax_role<D>(a, u, smem, sbase, tmem, warp >> 2, t0 * BN, n_tiles, !has_b, ctl);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == CT_MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TM_COLS);
     }
 }
 
@@ -404,7 +912,9 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Chunk
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, total = 0.f;
     if (M != -INFINITY) {
         for (int s = 0; s < a.n_split; ++s) {
-            const float w = ex2_approx(a.part_lse[s * rows + id] - M);
+            const float ls = a.part_lse[s * rows + id];
+            if (ls == -INFINITY) continue;  // a range that was not there, or that the row does not see
+            const float w = ex2_approx(ls - M);
             const float4 *src = reinterpret_cast<const float4 *>(a.part_o + (s * rows + id) * D + e0);
             const float4 x = src[0], y = src[1];
             total += w;
@@ -448,26 +958,54 @@ sfa_status check_attn(const sfa_cache_attn_desc *d)
 }
 
 struct Plan {
-    int row_tiles, n_split;
+    bool tiles;  // tile_attn_kernel, else rows_attn_kernel
+    int row_tiles, n_split, range_len;
     int64_t ctas;
 };
 
 constexpr int MAX_SPLIT = 64;
+constexpr int TILE_MIN_ROWS = 17;
 
 Plan plan_of(const sfa_cache_attn_desc *d, const sfa_cache *c)
 {
     Plan p;
     const int64_t rows = (int64_t)d->Lq * (d->H / d->H_kv);
-    p.row_tiles = (int)((rows + FR_ROWS - 1) / FR_ROWS);
+    p.tiles = rows >= TILE_MIN_ROWS;
+    const int tile_rows = p.tiles ? CT_ROWS : FR_ROWS, step_keys = p.tiles ? BN : FR_KEYS;
+    p.row_tiles = (int)((rows + tile_rows - 1) / tile_rows);
     const int64_t units = (int64_t)d->B * d->H_kv * p.row_tiles;
-    const int64_t kv = d->max_kv > 0 ? d->max_kv : (int64_t)c->table_len * c->page_len;
-    // four CTAs fit an SM: as many ranges as fill them once, each of at least 4 steps
-    int64_t s = (int64_t)attn_sms() * 4 / units;
-    const int64_t most = kv / (4 * FR_KEYS);
-    s = s < most ? s : most;
-    p.n_split = (int)(s < 1 ? 1 : s > MAX_SPLIT ? MAX_SPLIT : s);
+    int64_t kv = (int64_t)c->table_len * c->page_len;
+    if (d->max_kv > 0 && d->max_kv < kv) kv = d->max_kv;
+    const int64_t steps = std::max<int64_t>(1, (kv + step_keys - 1) / step_keys);
+    // Modelled as waves of equal ranges: a range costs its steps and a fixed start and end,
+    // and the joining kernel the partial results' bytes (in steps of a CTA's share).
+    const double slots = (double)attn_sms() * (p.tiles ? 1 : 4);
+    const double fixed = p.tiles ? 4.0 : 6.0;
+    const double step_us = p.tiles ? 2.4 : 1.6;
+    const double join_us = (double)d->B * d->H * d->Lq * (d->d + 1) * 4.0 / 5.0e6;
+    double best = 1e300;
+    p.n_split = 1;
+    for (int64_t k = 1; k <= MAX_SPLIT && k <= steps; ++k) {
+        const double len = (double)((steps + k - 1) / k);
+        const double us = std::ceil(units * k / slots) * (len + fixed) * step_us + (k > 1 ? 3.0 + (k + 1) * join_us : 0.0);
+        if (us < best) {
+            best = us;
+            p.n_split = (int)k;
+        }
+    }
+    p.range_len = (int)std::min<int64_t>((steps + p.n_split - 1) / p.n_split, 1 << 30);
     p.ctas = units * p.n_split;
     return p;
+}
+
+template <int D>
+sfa_status launch_tiles(const ChunkArgs &a, unsigned grid, cudaStream_t s)
+{
+    if (cudaFuncSetAttribute(tile_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM_BYTES) !=
+        cudaSuccess)
+        return SFA_ERR_CUDA;
+    tile_attn_kernel<D><<<grid, CT_THREADS, Cfg<D>::SMEM_BYTES, s>>>(a);
+    return launch_status();
 }
 
 size_t part_bytes(const sfa_cache_attn_desc *d, int n_split)
@@ -540,10 +1078,18 @@ extern "C" sfa_status sfa_forward_cache(const sfa_cache_attn_desc *d, const sfa_
     const int64_t rows = (int64_t)d->B * d->H * d->Lq;
     a.part_o = static_cast<float *>(workspace);
     a.part_lse = a.part_o ? a.part_o + (int64_t)p.n_split * rows * d->d : nullptr;
+    a.range_len = p.range_len;
+    a.timeout_ns = (uint64_t)(d->timeout_us ? d->timeout_us : DEFAULT_TIMEOUT_US) * 1000;
+    a.debug_flags = d->debug_flags;
     cudaStream_t s = as_cuda(stream);
-    if (d->d == 128) rows_attn_kernel<128><<<(unsigned)p.ctas, FR_WARPS * 32, 0, s>>>(a);
-    else rows_attn_kernel<64><<<(unsigned)p.ctas, FR_WARPS * 32, 0, s>>>(a);
-    st = launch_status();
+    const unsigned grid = (unsigned)p.ctas;
+    if (p.tiles) {
+        st = d->d == 128 ? launch_tiles<128>(a, grid, s) : launch_tiles<64>(a, grid, s);
+    } else {
+        if (d->d == 128) rows_attn_kernel<128><<<grid, FR_WARPS * 32, 0, s>>>(a);
+        else rows_attn_kernel<64><<<grid, FR_WARPS * 32, 0, s>>>(a);
+        st = launch_status();
+    }
     if (st != SFA_OK || p.n_split == 1) return st;
     cudaLaunchConfig_t cfg = {};
     const int per_cta = 128 / (d->d / 8);

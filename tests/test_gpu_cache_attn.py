@@ -282,3 +282,19 @@ def test_offsets_past_32_bits():
         o, l = m.forward_cache(q, cache, table, n)
         torch.cuda.synchronize()
         check(o[0, 0], l[0, 0], f64(q[0, 0]), back, back, 1 / math.sqrt(d), False)
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """The softmax withholds its first probabilities (a test hook): the waits run out after their
+    limit, the call reports it and returns, and the next call is right."""
+    m, q, cache, t, ln, o, l, args = run_case(B=1, H=2, Hk=2, L=300, d=128, P=32, kv=700)
+    for n in (300, 100):  # two query tiles, one
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        m.forward_cache(q[:, :, :n], cache, t, ln, dev_status=status, timeout_us=2000,
+                        debug_flags=m.SFA_DEBUG_STALL_SOFTMAX, **args)
+        torch.cuda.synchronize()
+        assert status.item() == m.SFA_ERR_TIMEOUT
+        status.zero_()
+        o2, l2 = m.forward_cache(q, cache, t, ln, dev_status=status, **args)
+        torch.cuda.synchronize()
+        assert status.item() == 0 and torch.equal(o2, o) and torch.equal(l2, l)
