@@ -81,6 +81,27 @@ __device__ __forceinline__ int64_t cache_row(const CacheView &c, int b, int h, i
     return ((int64_t)page * c.heads + (c.heads > 1 ? h : 0)) * c.page_len + ((uint32_t)j - slot * (uint32_t)c.page_len);
 }
 
+// The same in two steps, so that the page number can be on its way meanwhile: `open` reads it
+// (for a token that is not wanted, the row's first entry), `row` checks it.
+struct CachePlace {
+    int page, off;
+    bool wanted;
+    __device__ __forceinline__ void open(const CacheView &c, const int32_t *table_row, int j, bool want)
+    {
+        const uint32_t slot = want ? (uint32_t)j / (uint32_t)c.page_len : 0u;
+        wanted = want;
+        off = (int)((uint32_t)j - slot * (uint32_t)c.page_len);
+        page = __ldg(table_row + slot);
+    }
+    // pool row, or -1; a wanted token without a valid page is reported
+    __device__ __forceinline__ int row(const CacheView &c, int h, int32_t *status) const
+    {
+        const bool ok = wanted && page >= 0 && page < c.n_pages;
+        if (wanted && !ok) report_status(status, SFA_ERR_BAD_SET);
+        return ok ? (page * c.heads + (c.heads > 1 ? h : 0)) * c.page_len + off : -1;
+    }
+};
+
 // e of a block whose largest magnitude has the bf16 bits `amax` (finite, sign cleared): the
 // smallest e with amax <= 448 * 2^e = 1.75 * 2^(e + 8).  For amax = (1 + m / 128) * 2^E that
 // is E - 8, one more where m > 96; adding 31 carries into the exponent field exactly then.
@@ -103,6 +124,22 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
     uint32_t r;
     asm("mul.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
+}
+
+// 16 or 8 bytes of codes, read once: kept out of L1, where the page tables stay
+__device__ __forceinline__ uint4 load_codes16(const uint8_t *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 load_codes8(const uint8_t *p)
+{
+    uint2 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
 }
 
 // Codes to bf16.  Each 16-bit half of x holds one code twice (byte permutation of the caller);

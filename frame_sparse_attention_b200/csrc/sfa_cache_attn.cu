@@ -120,11 +120,14 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint4 &a, uint32_
         : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
-// codes j and j + 1 (j = 0 or 2) of a word -> bf16 pair times f
-template <int J>
-__device__ __forceinline__ uint32_t codes_in_word(uint32_t w, uint32_t f)
+// The four codes of a word -> two bf16 pairs times f.  In bf16's place a code is its sign, then
+// four zero bits, then its other seven bits: the low bytes of the four halves and the high ones
+// are formed for the whole word and dealt out.
+__device__ __forceinline__ void codes_of_word(uint32_t w, uint32_t f, uint32_t &p0, uint32_t &p1)
 {
-    return mul_bf16x2(spread_codes(__byte_perm(w, 0, J ? 0x3322 : 0x1100)), f);
+    const uint32_t lo = (w << 4) & 0xf0f0f0f0u, hi = (w & 0x80808080u) | ((w >> 4) & 0x07070707u);
+    p0 = mul_bf16x2(__byte_perm(lo, hi, 0x5140), f);
+    p1 = mul_bf16x2(__byte_perm(lo, hi, 0x7362), f);
 }
 // code j of words lo and hi -> bf16 pair times f
 __device__ __forceinline__ uint32_t codes_of_two(uint32_t lo, uint32_t hi, int j, uint32_t f)
@@ -132,6 +135,14 @@ __device__ __forceinline__ uint32_t codes_of_two(uint32_t lo, uint32_t hi, int j
     const uint32_t sel = (uint32_t)j * 0x1111u + 0x4400u;
     return mul_bf16x2(spread_codes(__byte_perm(lo, hi, sel)), f);
 }
+
+// compile-time answers for the code paths of large scales
+struct Yes {
+    static constexpr bool value = true;
+};
+struct No {
+    static constexpr bool value = false;
+};
 
 template <int D>
 struct ScaleWord;
@@ -198,59 +209,55 @@ __global__ void __launch_bounds__(FR_WARPS * 32, 4) rows_attn_kernel(const __gri
         for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // of rows g and g + 8
 
-    // pool row of key (16 of them: lanes 0-15, repeated in 16-31) of step s, -1 past the end
-    auto rows_of = [&](int s) -> int {
+    // place of key (16 of them: lanes 0-15, repeated in 16-31) of step s
+    const int32_t *table = a.cache.table + u.b * a.cache.ts0 + u.hk * a.cache.ts1;
+    CachePlace place;
+    auto look_up = [&](int s) {
         const int j = s * FR_KEYS + warp * 16 + (lane & 15);
-        if (s >= s1 || j >= seen) return -1;
-        const int64_t r = cache_row(a.cache, u.b, u.hk, j);
-        if (r < 0) report_status(a.status, SFA_ERR_BAD_SET);
-        return (int)r;
+        place.open(a.cache, table, j, s < s1 && j < seen);
     };
     uint4 kr[2][KC];
-    uint32_t vr[4][VW], ksc[2], vsc[4];
+    uint32_t vr[4][VW], kf[2], vf[4];  // codes and scales of this lane's K and V rows
+    uint32_t absent = 0u;              // bits 0, 1: of K, bits 2 .. 5: of V, the row is not there
     const scale_t *k_scale = reinterpret_cast<const scale_t *>(a.cache.k_scale);
     const scale_t *v_scale = reinterpret_cast<const scale_t *>(a.cache.v_scale);
+    // Rows that are not there read row 0 of the pool and get the scale byte 0, which makes any
+    // code a finite number: their keys are masked and their probabilities 0.
     auto load_k = [&](int rows) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int r = __shfl_sync(0xffffffffu, rows, g + 8 * s);
-            ksc[s] = r >= 0 ? (uint32_t)__ldg(k_scale + r) : 0u;
+            int r = __shfl_sync(0xffffffffu, rows, g + 8 * s);
+            absent = (absent & ~(1u << s)) | (r < 0 ? 1u << s : 0u);
+            r = max(r, 0);
+            kf[s] = (uint32_t)__ldg(k_scale + r);
 #pragma unroll
-            for (int c = 0; c < KC; ++c)
-                kr[s][c] = r >= 0 ? __ldg(reinterpret_cast<const uint4 *>(a.cache.k + (int64_t)r * D + c * 64 + t * 16))
-                                  : make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < KC; ++c) kr[s][c] = load_codes16(a.cache.k + (int64_t)r * D + c * 64 + t * 16);
         }
     };
     auto load_v = [&](int rows) {
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            const int r = __shfl_sync(0xffffffffu, rows, 2 * t + (s & 1) + (s >> 1) * 8);
-            vsc[s] = r >= 0 ? (uint32_t)__ldg(v_scale + r) : 0u;
+            int r = __shfl_sync(0xffffffffu, rows, 2 * t + (s & 1) + (s >> 1) * 8);
+            absent = (absent & ~(4u << s)) | (r < 0 ? 4u << s : 0u);
+            r = max(r, 0);
+            vf[s] = (uint32_t)__ldg(v_scale + r);
             const uint8_t *p = a.cache.v + (int64_t)r * D + g * NT;
             if (D == 128) {
-                const uint4 x = r >= 0 ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0u, 0u, 0u, 0u);
+                const uint4 x = load_codes16(p);
                 vr[s][0] = x.x, vr[s][1] = x.y, vr[s][VW - 2] = x.z, vr[s][VW - 1] = x.w;
             } else {
-                const uint2 x = r >= 0 ? __ldg(reinterpret_cast<const uint2 *>(p)) : make_uint2(0u, 0u);
+                const uint2 x = load_codes8(p);
                 vr[s][0] = x.x, vr[s][1] = x.y;
             }
         }
     };
 
-    int rows = rows_of(s0);
+    look_up(s0);
+    int rows = place.row(a.cache, u.hk, a.status);
     load_k(rows);
     load_v(rows);
-    for (int st = s0; st < s1; ++st) {
-        const int rows_next = rows_of(st + 1);
-        // scales of the block each register lies in; 2^e beyond bf16's range in one step (e > 7,
-        // values of 57344 and more) takes a second product
-        bool two = false;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) two |= __vcmpgtu4(ksc[s], 0x01010101u * SCALE_ONE_STEP) != 0u;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) two |= __vcmpgtu4(vsc[s], 0x01010101u * SCALE_ONE_STEP) != 0u;
-        two = __any_sync(0xffffffffu, two);
-
+    look_up(s0 + 1);
+    auto step = [&](auto two, int st, int rows_next) {
         // ---- S = Q K^T, keys 8 s + 2 t + {0, 1} of rows g, g + 8
         float sc[2][4];
 #pragma unroll
@@ -262,7 +269,7 @@ __global__ void __launch_bounds__(FR_WARPS * 32, 4) rows_attn_kernel(const __gri
             uint32_t f[2], r2[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const uint32_t byte = (ksc[s] >> (8 * (2 * c + (t >> 1)))) & 0xffu;
+                const uint32_t byte = (kf[s] >> (8 * (2 * c + (t >> 1)))) & 0xffu;
                 f[s] = scale_bits(byte) * 0x10001u;
                 r2[s] = scale_rest_bits(byte) * 0x10001u;
             }
@@ -272,8 +279,9 @@ __global__ void __launch_bounds__(FR_WARPS * 32, 4) rows_attn_kernel(const __gri
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     const uint32_t kw = w == 0 ? kr[s][c].x : w == 1 ? kr[s][c].y : w == 2 ? kr[s][c].z : kr[s][c].w;
-                    uint32_t b0 = codes_in_word<0>(kw, f[s]), b1 = codes_in_word<2>(kw, f[s]);
-                    if (two) {
+                    uint32_t b0, b1;
+                    codes_of_word(kw, f[s], b0, b1);
+                    if (decltype(two)::value) {
                         b0 = mul_bf16x2(b0, r2[s]);
                         b1 = mul_bf16x2(b1, r2[s]);
                     }
@@ -339,21 +347,39 @@ __global__ void __launch_bounds__(FR_WARPS * 32, 4) rows_attn_kernel(const __gri
 
         // ---- O += P V
         const int blk = (g * NT) / CACHE_BLOCK * 8;
-        uint32_t f01 = scale_bits((vsc[0] >> blk) & 0xffu) | (scale_bits((vsc[1] >> blk) & 0xffu) << 16);
-        uint32_t f23 = scale_bits((vsc[2] >> blk) & 0xffu) | (scale_bits((vsc[3] >> blk) & 0xffu) << 16);
-        uint32_t r01 = scale_rest_bits((vsc[0] >> blk) & 0xffu) | (scale_rest_bits((vsc[1] >> blk) & 0xffu) << 16);
-        uint32_t r23 = scale_rest_bits((vsc[2] >> blk) & 0xffu) | (scale_rest_bits((vsc[3] >> blk) & 0xffu) << 16);
+        uint32_t f01 = scale_bits((vf[0] >> blk) & 0xffu) | (scale_bits((vf[1] >> blk) & 0xffu) << 16);
+        uint32_t f23 = scale_bits((vf[2] >> blk) & 0xffu) | (scale_bits((vf[3] >> blk) & 0xffu) << 16);
+        uint32_t r01 = scale_rest_bits((vf[0] >> blk) & 0xffu) | (scale_rest_bits((vf[1] >> blk) & 0xffu) << 16);
+        uint32_t r23 = scale_rest_bits((vf[2] >> blk) & 0xffu) | (scale_rest_bits((vf[3] >> blk) & 0xffu) << 16);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             uint32_t b0 = codes_of_two(vr[0][i / 4], vr[1][i / 4], i % 4, f01);
             uint32_t b1 = codes_of_two(vr[2][i / 4], vr[3][i / 4], i % 4, f23);
-            if (two) {
+            if (decltype(two)::value) {
                 b0 = mul_bf16x2(b0, r01);
                 b1 = mul_bf16x2(b1, r23);
             }
             mma_16816(o[i], p, b0, b1);
         }
         load_v(rows_next);
+    };
+    for (int st = s0; st < s1; ++st) {
+        const int rows_next = place.row(a.cache, u.hk, a.status);
+        look_up(st + 2);
+        if (absent) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) kf[s] = (absent >> s) & 1u ? 0u : kf[s];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) vf[s] = (absent >> (2 + s)) & 1u ? 0u : vf[s];
+        }
+        // 2^e beyond bf16's range in one step (e > 7, values of 57344 and more) takes a second product
+        bool two = false;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) two |= __vcmpgtu4(kf[s], 0x01010101u * SCALE_ONE_STEP) != 0u;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) two |= __vcmpgtu4(vf[s], 0x01010101u * SCALE_ONE_STEP) != 0u;
+        if (__any_sync(0xffffffffu, two)) step(Yes{}, st, rows_next);
+        else step(No{}, st, rows_next);
     }
 
     // ---- join the warps: every warp's O against the common max, then the sum of four
@@ -414,19 +440,57 @@ __global__ void __launch_bounds__(FR_WARPS * 32, 4) rows_attn_kernel(const __gri
 }
 
 // ----------------------------------------------------------------- many query rows
-// Units of two 128-row query tiles against 128-key tiles, on the tensor cores through tensor
-// memory, in the schedule of the frame-list forward kernel (S one tile ahead of the softmax,
-// P V behind it; a unit with one query tile runs S two key tiles ahead).  What differs is how
-// the operands arrive: four warps load the codes of a K and a V tile into registers, a tile
-// ahead, look up their pages, and store them as bf16 in the 128-byte-swizzled layout that
-// the matrix instruction reads, zeros behind the last key; the softmax warps bring their own
-// query rows, since a unit's rows may be those of several heads.
+// Units of two 128-row query tiles A and B against 128-key tiles, on the tensor cores:
+//   S_A(0) S_B(0) | P V_A(j) S_A(j+1) | P V_B(j) S_B(j+1) | ...
+// While the softmax of one query tile runs, the tensor cores work on the other.  A unit with
+// one query tile has both tiles' S buffers to itself and keeps S one key tile ahead:
+//   S(0) S(1) | P V(j) S(j+2) | ...
+// Seven warps load the codes of the K and V tiles into registers, look up the pages of the
+// next tile meanwhile, and store them as bf16 in the 128-byte-swizzled layout that the matrix
+// instruction reads, zeros behind the last key; the softmax warps bring their own query rows,
+// since a unit's rows may be those of several heads.
+// Shared memory is what this kernel runs short of: a 128 x 128 x 16 product with both
+// operands there takes all of its bandwidth, and the converted tiles have to get in as well
+// (with P in shared memory, as in the frame-list kernel, a key tile took 5600 cycles, 2200 of
+// them in the issue of 11 loads behind blocked stores).  So P stays in tensor memory, in the
+// columns of the S that it comes from, as the first operand of P V.
 constexpr int CT_SOFTMAX_WARPS = 8;       // warps 0-3: query tile A, 4-7: B
-constexpr int CT_CONV_WARP = 8;           // 8-11: codes to bf16
-constexpr int CT_CONV_WARPS = 4;
-constexpr int CT_MMA_WARP = 12;
-constexpr int CT_THREADS = 32 * (CT_MMA_WARP + 1);
+constexpr int CT_K_WARP = 8;              // 8-11: codes of K to bf16
+constexpr int CT_V_WARP = 12;             // 12-14: of V
+constexpr int CT_MMA_WARP = 15;
+constexpr int CT_K_WARPS = CT_V_WARP - CT_K_WARP, CT_V_WARPS = CT_MMA_WARP - CT_V_WARP;
+constexpr int CT_THREADS = 512;           // four warps to a scheduler: 128 registers a thread
 constexpr int CT_ROWS = 2 * BM;
+
+template <int D>
+struct CCfg {
+    static constexpr int TILE_BYTES = BM * D * 2;  // one Q, K or V tile in bf16
+    static constexpr int NSK = 2, NSV = 2;
+    static constexpr int SMEM_Q = 0;               // query tiles A and B, then their output rows
+    static constexpr int SMEM_K = 2 * TILE_BYTES;
+    static constexpr int SMEM_V = SMEM_K + NSK * TILE_BYTES;
+    static constexpr int SMEM_BAR = SMEM_V + NSV * TILE_BYTES;
+    static constexpr int SMEM_BYTES = SMEM_BAR + 256 + 1024;  // + barriers, + alignment slack
+};
+
+// mbarriers (8 bytes each) at SMEM_BAR
+template <int D>
+struct CBars {
+    uint32_t base;
+    static constexpr int NSK = CCfg<D>::NSK, NSV = CCfg<D>::NSV;
+    __device__ uint32_t k_full(int s) const { return base + 8 * s; }
+    __device__ uint32_t k_free(int s) const { return base + 8 * (NSK + s); }
+    __device__ uint32_t v_full(int s) const { return base + 8 * (2 * NSK + s); }
+    __device__ uint32_t v_free(int s) const { return base + 8 * (2 * NSK + NSV + s); }
+    __device__ uint32_t s_full(int x) const { return base + 8 * (2 * NSK + 2 * NSV + x); }      // S of tile x
+    __device__ uint32_t p_full(int x) const { return base + 8 * (2 * NSK + 2 * NSV + 2 + x); }  // P of tile x
+    __device__ uint32_t q_full() const { return base + 8 * (2 * NSK + 2 * NSV + 4); }
+    __device__ uint32_t o_final() const { return base + 8 * (2 * NSK + 2 * NSV + 5); }  // after the last P V
+    __device__ uint32_t pv_done() const { return base + 8 * (2 * NSK + 2 * NSV + 6); }  // one-tile units: a P V
+    __device__ uint32_t drain() const { return base + 8 * (2 * NSK + 2 * NSV + 7); }
+    static constexpr int COUNT = 2 * NSK + 2 * NSV + 8;
+    static_assert(8 * COUNT <= 160, "mbarriers end before the flags at +160");
+};
 
 // byte offset of the 16-byte piece `ch` (8 elements) of row r in a swizzled tile
 template <int D>
@@ -435,182 +499,180 @@ __device__ __forceinline__ uint32_t swz(int r, int ch)
     return (uint32_t)((ch >> 3) * Cfg<D>::BOX_BYTES + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
 }
 
-// The K and V tiles of the unit, codes to bf16.  Warp w takes rows 32 w .. 32 w + 31 of every
-// tile: lane l looks up row l's place, D/16 lanes then share a row, 16 codes each.
-template <int D>
+// The K (IS_K) or V tiles of the unit, codes to bf16.  D/16 lanes share a row, 16 codes each,
+// and the tile's rows go round the warps, RPI at a time.  A lane looks up one row's place (two
+// where a warp has more than 32 rows).  The next tile's codes are on their way while the warp
+// waits for its slot.
+template <int D, bool IS_K>
 __device__ void convert_role(const ChunkArgs &a, const Unit &u, uint32_t sbase, int key0, int key_end, int n_tiles,
                              const Ctl &ctl)
 {
-    using C = Cfg<D>;
-    constexpr int LR = D / 16;        // lanes per row
-    constexpr int RPI = 32 / LR;      // rows per load of the warp
-    constexpr int NI = 32 / RPI;      // loads per tile
+    using C = CCfg<D>;
+    constexpr int NS = IS_K ? C::NSK : C::NSV;
+    constexpr int NW = IS_K ? CT_K_WARPS : CT_V_WARPS;
+    constexpr int LR = D / 16;                         // lanes per row
+    constexpr int RPI = 32 / LR;                       // rows per load of the warp
+    constexpr int NI = (BN / RPI + NW - 1) / NW;       // loads per tile
+    constexpr int LK = (NI * RPI + 31) / 32;           // places that a lane looks up
     typedef typename ScaleWord<D>::type scale_t;
-    const Bars<D> bar{sbase + C::SMEM_BAR};
-    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - CT_CONV_WARP;
+    const CBars<D> bar{sbase + C::SMEM_BAR};
+    const uint8_t *codes = IS_K ? a.cache.k : a.cache.v;
+    const scale_t *scales = reinterpret_cast<const scale_t *>(IS_K ? a.cache.k_scale : a.cache.v_scale);
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - (IS_K ? CT_K_WARP : CT_V_WARP);
     const int sub = lane / LR, c = lane % LR;
-
-    auto rows_of = [&](int j) -> int {  // pool row of key 32 w + lane of tile j
-        const int key = key0 + j * BN + w * 32 + lane;
-        if (j >= n_tiles || key >= key_end) return -1;
-        const int64_t r = cache_row(a.cache, u.b, u.hk, key);
-        if (r < 0) report_status(a.status, SFA_ERR_BAD_SET);
-        return (int)r;
-    };
-    auto load = [&](const uint8_t *codes, const uint8_t *scales, int rows, uint4 (&x)[NI], uint32_t &sw) {
-        sw = rows >= 0 ? (uint32_t)__ldg(reinterpret_cast<const scale_t *>(scales) + rows) : 0u;
+    const int32_t *table = a.cache.table + u.b * a.cache.ts0 + u.hk * a.cache.ts1;
+    uint4 x[NI];
+    uint32_t sw[LK], there = 0u;  // scales of this lane's rows; bit i: the row of x[i] is there
+    CachePlace place[LK];         // of this lane's keys in the next tile to load
+    auto look_up = [&](int j) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int r = __shfl_sync(0xffffffffu, rows, i * RPI + sub);
-            x[i] = r >= 0 ? __ldg(reinterpret_cast<const uint4 *>(codes + (int64_t)r * D + c * 16))
-                          : make_uint4(0u, 0u, 0u, 0u);
+        for (int k = 0; k < LK; ++k) {
+            const int q = k * 32 + lane, row = (q / RPI * NW + w) * RPI + q % RPI;  // this warp's q-th row
+            const int key = key0 + j * BN + row;
+            place[k].open(a.cache, table, key, j < n_tiles && row < BN && key < key_end);
         }
     };
-    auto store = [&](uint32_t tile, const uint4 (&x)[NI], uint32_t sw) {
-        const bool two = __any_sync(0xffffffffu, __vcmpgtu4(sw, 0x01010101u * SCALE_ONE_STEP) != 0u);
+    // Rows that are not there read row 0 of the pool, and count as zeros by their factor: no
+    // branch parts the loads.
+    auto load = [&]() {
+        int rows[LK];
+#pragma unroll
+        for (int k = 0; k < LK; ++k) rows[k] = place[k].row(a.cache, u.hk, a.status);
+        there = 0u;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int r = i * RPI + sub;  // row inside this warp's 32
-            const uint32_t byte = (__shfl_sync(0xffffffffu, sw, r) >> (8 * (c / 2))) & 0xffu;
-            const uint32_t f = scale_bits(byte) * 0x10001u;
-            const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            const int r = __shfl_sync(0xffffffffu, rows[i * RPI / 32], (i * RPI + sub) & 31);
+            there |= (r >= 0 ? 1u : 0u) << i;
+            x[i] = load_codes16(codes + (int64_t)max(r, 0) * D + c * 16);
+        }
+#pragma unroll
+        for (int k = 0; k < LK; ++k) sw[k] = (uint32_t)__ldg(scales + max(rows[k], 0));
+    };
+    uint32_t present = 0u;  // `there` of the tile that is being converted
+    // codes of x[i] -> eight bf16 pairs; TWO: exponents above 7 somewhere in the warp's rows
+    auto convert = [&](auto two, int i, uint32_t byte, uint32_t (&y)[8]) {
+        const uint32_t f = (present >> i) & 1u ? scale_bits(byte) * 0x10001u : 0u;
+        codes_of_word(x[i].x, f, y[0], y[1]);
+        codes_of_word(x[i].y, f, y[2], y[3]);
+        codes_of_word(x[i].z, f, y[4], y[5]);
+        codes_of_word(x[i].w, f, y[6], y[7]);
+        if (decltype(two)::value) {
+            const uint32_t g = scale_rest_bits(byte) * 0x10001u;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = mul_bf16x2(y[k], g);
+        }
+    };
+    // the upper half of a 128-element row's lanes store their two pieces in the other order, so
+    // that the eight lanes of one access fall on all eight 16-byte bank groups
+    const bool swap = D == 128 && c >= 4;
+    auto store = [&](uint32_t tile, int i, const uint32_t (&y)[8]) {
+        const int row = (i * NW + w) * RPI + sub;
+        if (row < BN) {
+            const uint32_t first[4] = {swap ? y[4] : y[0], swap ? y[5] : y[1], swap ? y[6] : y[2], swap ? y[7] : y[3]};
+            const uint32_t second[4] = {swap ? y[0] : y[4], swap ? y[1] : y[5], swap ? y[2] : y[6], swap ? y[3] : y[7]};
+            st_shared_v4(tile + swz<D>(row, 2 * c + (swap ? 1 : 0)), first);
+            st_shared_v4(tile + swz<D>(row, 2 * c + (swap ? 0 : 1)), second);
+        }
+    };
+    auto one_tile = [&](auto two, int j) -> bool {
+        const int s = j % NS, use = j / NS;
+        const uint32_t tile = sbase + (IS_K ? C::SMEM_K : C::SMEM_V) + s * C::TILE_BYTES;
+        uint32_t byte[NI];
+        present = there;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            byte[i] = (__shfl_sync(0xffffffffu, sw[i * RPI / 32], (i * RPI + sub) & 31) >> (8 * (c / 2))) & 0xffu;
+        if (use > 0 &&
+            !__all_sync(0xffffffffu, wait_bar(IS_K ? bar.k_free(s) : bar.v_free(s), (use - 1) & 1, ctl)))
+            return false;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
             uint32_t y[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                y[2 * k] = codes_in_word<0>(in[k], f);
-                y[2 * k + 1] = codes_in_word<2>(in[k], f);
-            }
-            if (two) {
-                const uint32_t g = scale_rest_bits(byte) * 0x10001u;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = mul_bf16x2(y[k], g);
-            }
-            const uint32_t lo[4] = {y[0], y[1], y[2], y[3]}, hi[4] = {y[4], y[5], y[6], y[7]};
-            // the upper half of a row's lanes store their two pieces in the other order, so that
-            // the eight lanes of one access fall on all eight 16-byte bank groups
-            const bool swap = D == 128 && c >= 4;
-            const int row = w * 32 + r;
-            st_shared_v4(tile + swz<D>(row, 2 * c + (swap ? 1 : 0)), swap ? hi : lo);
-            st_shared_v4(tile + swz<D>(row, 2 * c + (swap ? 0 : 1)), swap ? lo : hi);
+            convert(two, i, byte[i], y);
+            store(tile, i, y);
         }
+        load();
         fence_proxy_async_smem();
         __syncwarp();
+        if (lane == 0) mbar_arrive(IS_K ? bar.k_full(s) : bar.v_full(s));
+        return true;
     };
-
-    uint4 kx[NI], vx[NI];
-    uint32_t ks, vs;
-    int rows_k = rows_of(0), rows_v;
-    load(a.cache.k, a.cache.k_scale, rows_k, kx, ks);
-    load(a.cache.v, a.cache.v_scale, rows_k, vx, vs);
-    // K(0) | K(j + 1) V(j) | ...
-    for (int j = -1; j < n_tiles; ++j) {
-        if (j + 1 < n_tiles) {
-            const int s = (j + 1) % C::NSK, use = (j + 1) / C::NSK;
-            if (use > 0 && !__all_sync(0xffffffffu, wait_bar(bar.k_free(s), (use - 1) & 1, ctl))) return;
-            store(sbase + C::SMEM_K + s * C::TILE_BYTES, kx, ks);
-            if (lane == 0) mbar_arrive(bar.k_full(s));
-            rows_v = rows_k;  // of tile j + 1, for its V
-            rows_k = rows_of(j + 2);
-            load(a.cache.k, a.cache.k_scale, rows_k, kx, ks);
-        } else {
-            rows_v = -1;
-        }
-        if (j >= 0) {
-            const int s = j % C::NSV, use = j / C::NSV;
-            if (use > 0 && !__all_sync(0xffffffffu, wait_bar(bar.v_free(s), (use - 1) & 1, ctl))) return;
-            store(sbase + C::SMEM_V + s * C::TILE_BYTES, vx, vs);
-            if (lane == 0) mbar_arrive(bar.v_full(s));
-            load(a.cache.v, a.cache.v_scale, rows_v, vx, vs);
-        }
+    look_up(0);
+    load();
+    look_up(1);
+    for (int j = 0; j < n_tiles; ++j) {
+        bool two = false;
+#pragma unroll
+        for (int k = 0; k < LK; ++k) two |= __vcmpgtu4(sw[k], 0x01010101u * SCALE_ONE_STEP) != 0u;
+        const bool go = __any_sync(0xffffffffu, two) ? one_tile(Yes{}, j) : one_tile(No{}, j);
+        if (!go) return;
+        look_up(j + 2);
     }
 }
 
+// O[128 x D] += P[128 x 128] V[128 x D], P in tensor memory (8 columns per 16 keys), V MN-major
 template <int D>
-__device__ void chunk_mma_pair(uint32_t sbase, uint32_t tmem, int n_tiles, const Ctl &ctl)
+__device__ __forceinline__ void issue_pv_tmem(uint32_t t_o, uint32_t t_p, uint64_t dv, bool accumulate)
 {
-    using C = Cfg<D>;
-    constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, false);
-    const Bars<D> bar{sbase + C::SMEM_BAR};
-    const uint64_t dq = sdesc_sw128(sbase + C::SMEM_Q, 16, 1024), dk = sdesc_sw128(sbase + C::SMEM_K, 16, 1024);
-    const uint64_t dv = sdesc_sw128(sbase + C::SMEM_V, C::BOX_BYTES, 1024), dp = sdesc_sw128(sbase + C::SMEM_P, 16, 1024);
-    bool issued = false;
-    if (!__all_sync(0xffffffffu, wait_bar(bar.q_full(), 0, ctl))) goto done;
-    if (!__all_sync(0xffffffffu, wait_bar(bar.k_full(0), 0, ctl))) goto done;
-    tc_fence_after();
-    for (int x = 0; x < 2; ++x) {
-        issue_s<D>(tmem + tcol_s(x), desc_add(dq, x * C::TILE_BYTES), dk, idesc_s);
-        commit_one(bar.s_full(x));
+    constexpr uint32_t idesc = idesc_bf16_f32(BM, D, true);
+    if (elect_one()) {
+#pragma unroll
+        for (uint32_t kk = 0; kk < BN / 16; ++kk)
+            mma_ts(t_o, t_p + 8 * kk, desc_add(dv, kk * 2048), idesc, (accumulate || kk > 0) ? 1u : 0u);
     }
-    commit_one(bar.k_free(0));
-    issued = true;
+    __syncwarp();
+}
+
+// The tensor-core schedule (one warp, one elected lane): see above.  With two query tiles
+// (PAIR) buffer x is tile x's and takes every key tile; with one, buffer j & 1 takes key tile
+// j, and a buffer's next S is two key tiles on.
+template <int D, bool PAIR>
+__device__ void chunk_mma(uint32_t sbase, uint32_t tmem, int n_tiles, const Ctl &ctl)
+{
+    using C = CCfg<D>;
+    constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, false);
+    const CBars<D> bar{sbase + C::SMEM_BAR};
+    const uint64_t dq = sdesc_sw128(sbase + C::SMEM_Q, 16, 1024), dk = sdesc_sw128(sbase + C::SMEM_K, 16, 1024);
+    const uint64_t dv = sdesc_sw128(sbase + C::SMEM_V, Cfg<D>::BOX_BYTES, 1024);
+    bool issued = false;
+    // S of key tile j into buffer x (the K slot is free after its last reader)
+    auto s_into = [&](int x, int j, bool last_reader) {
+        const int sk = j % C::NSK;
+        issue_s<D>(tmem + tcol_s(x), desc_add(dq, PAIR ? x * C::TILE_BYTES : 0), desc_add(dk, sk * C::TILE_BYTES), idesc_s);
+        commit_one(bar.s_full(x));
+        if (last_reader) commit_one(bar.k_free(sk));
+        issued = true;
+    };
+    if (!__all_sync(0xffffffffu, wait_bar(bar.q_full(), 0, ctl))) goto done;
+    for (int x = 0; x < 2; ++x) {
+        const int j = PAIR ? 0 : x;
+        if (j >= n_tiles) break;
+        if ((!PAIR || x == 0) && !__all_sync(0xffffffffu, wait_bar(bar.k_full(j % C::NSK), (j / C::NSK) & 1, ctl))) goto done;
+        tc_fence_after();
+        s_into(x, j, !PAIR || x == 1);
+    }
     for (int j = 0; j < n_tiles; ++j) {
-        const int sv = j % C::NSV, sk = (j + 1) % C::NSK;
-        for (int x = 0; x < 2; ++x) {
-            if (!__all_sync(0xffffffffu, wait_bar(bar.p_full(x), j & 1, ctl))) goto done;
-            if (j + 1 < n_tiles) {
-                if (x == 0 && !__all_sync(0xffffffffu, wait_bar(bar.k_full(sk), ((j + 1) / C::NSK) & 1, ctl))) goto done;
-                tc_fence_after();
-                issue_s<D>(tmem + tcol_s(x), desc_add(dq, x * C::TILE_BYTES), desc_add(dk, sk * C::TILE_BYTES), idesc_s);
-                commit_one(bar.s_full(x));
-                if (x == 1) commit_one(bar.k_free(sk));
-            }
-            if (x == 0 && !__all_sync(0xffffffffu, wait_bar(bar.v_full(sv), (j / C::NSV) & 1, ctl))) goto done;
+        const int sv = j % C::NSV, jn = PAIR ? j + 1 : j + 2;
+        for (int i = 0; i < (PAIR ? 2 : 1); ++i) {
+            const int x = PAIR ? i : j & 1;
+            if (!__all_sync(0xffffffffu, wait_bar(bar.p_full(x), (PAIR ? j : j >> 1) & 1, ctl))) goto done;
+            if (i == 0 && !__all_sync(0xffffffffu, wait_bar(bar.v_full(sv), (j / C::NSV) & 1, ctl))) goto done;
             tc_fence_after();
-            issue_pv<D>(tmem + tcol_o(x), desc_add(dp, x * C::P_BYTES), desc_add(dv, sv * C::TILE_BYTES), BN, j > 0);
-            commit_one(bar.pv_x(x));
-            if (x == 1) {
+            issue_pv_tmem<D>(tmem + tcol_o(PAIR ? x : 0), tmem + tcol_s(x), desc_add(dv, sv * C::TILE_BYTES), j > 0);
+            if (!PAIR) commit_one(bar.pv_done());
+            if (!PAIR || i == 1) {
                 commit_one(bar.v_free(sv));
                 if (j == n_tiles - 1) commit_one(bar.o_final());
+            }
+            if (jn < n_tiles) {
+                if (i == 0 && !__all_sync(0xffffffffu, wait_bar(bar.k_full(jn % C::NSK), (jn / C::NSK) & 1, ctl))) goto done;
+                tc_fence_after();
+                s_into(x, jn, !PAIR || i == 1);
             }
         }
     }
 done:
     if (__any_sync(0xffffffffu, *ctl.abort != 0) && issued) {  // the tensor cores finish before TMEM is released
-        commit_one(bar.drain());
-        wait_drain(bar.drain(), 0);
-    }
-    __syncwarp();
-}
-
-template <int D>
-__device__ void chunk_mma_single(uint32_t sbase, uint32_t tmem, int n_tiles, const Ctl &ctl)
-{
-    using C = Cfg<D>;
-    constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, false);
-    const Bars<D> bar{sbase + C::SMEM_BAR};
-    const uint64_t dq = sdesc_sw128(sbase + C::SMEM_Q, 16, 1024), dk = sdesc_sw128(sbase + C::SMEM_K, 16, 1024);
-    const uint64_t dv = sdesc_sw128(sbase + C::SMEM_V, C::BOX_BYTES, 1024), dp = sdesc_sw128(sbase + C::SMEM_P, 16, 1024);
-    bool issued = false;
-    if (!__all_sync(0xffffffffu, wait_bar(bar.q_full(), 0, ctl))) goto done;
-    for (int j = 0; j < 2 && j < n_tiles; ++j) {
-        const int sk = j % C::NSK;
-        if (!__all_sync(0xffffffffu, wait_bar(bar.k_full(sk), (j / C::NSK) & 1, ctl))) goto done;
-        tc_fence_after();
-        issue_s<D>(tmem + tcol_s(j), dq, desc_add(dk, sk * C::TILE_BYTES), idesc_s);
-        commit_one(bar.s_full(j));
-        commit_one(bar.k_free(sk));
-        issued = true;
-    }
-    for (int j = 0; j < n_tiles; ++j) {
-        const int bj = j & 1, sv = j % C::NSV;
-        if (!__all_sync(0xffffffffu, wait_bar(bar.p_full(bj), (j >> 1) & 1, ctl))) goto done;
-        if (!__all_sync(0xffffffffu, wait_bar(bar.v_full(sv), (j / C::NSV) & 1, ctl))) goto done;
-        tc_fence_after();
-        issue_pv<D>(tmem + tcol_o(0), desc_add(dp, bj * C::P_BYTES), desc_add(dv, sv * C::TILE_BYTES), BN, j > 0);
-        commit_one(bar.pv_done());
-        commit_one(bar.v_free(sv));
-        if (j == n_tiles - 1) commit_one(bar.o_final());
-        if (j + 2 < n_tiles) {
-            const int sk = (j + 2) % C::NSK;
-            if (!__all_sync(0xffffffffu, wait_bar(bar.k_full(sk), ((j + 2) / C::NSK) & 1, ctl))) goto done;
-            tc_fence_after();
-            issue_s<D>(tmem + tcol_s(bj), dq, desc_add(dk, sk * C::TILE_BYTES), idesc_s);
-            commit_one(bar.s_full(bj));
-            commit_one(bar.k_free(sk));
-        }
-    }
-done:
-    if (__any_sync(0xffffffffu, *ctl.abort != 0) && issued) {
         commit_one(bar.drain());
         wait_drain(bar.drain(), 0);
     }
@@ -627,83 +689,65 @@ __device__ __forceinline__ void hide_columns(int c, int nv, uint32_t (&r)[32])
     }
 }
 
-// One key tile of the online softmax, as softmax_tile of the frame-list kernel, for rows that
-// see columns [0, nv) of the tile each (MASK; all of them otherwise).  m_used stays -inf, and
-// the row's probabilities 0, until the row has seen a key.
+// One key tile of the online softmax for this thread's row (thread = TMEM lane) that sees the
+// columns [0, nv) of it (MASK; all of them otherwise): the row's maximum first, then
+// P = exp2(S * scale * log2e - m) as bf16 over the columns that S has been read from.  m is
+// kept while it is at most 2^8 behind the maximum, else O and the row sum are rescaled; it
+// stays -inf, and the row's probabilities 0, until the row has seen a key.  P V of the key
+// tile before is complete: S of this one came after it, or (one-tile units) pv_done says so.
 template <int D, bool MASK>
-__device__ __forceinline__ bool chunk_softmax_tile(uint32_t t_s, uint32_t p_row, int row, uint32_t t_o, int nv, float sl2,
-                                                   float &m_used, float &l, int j, uint32_t pv_done, uint32_t pv_first,
-                                                   const Ctl &ctl)
+__device__ __forceinline__ bool chunk_softmax_tile(uint32_t t_s, uint32_t t_o, int nv, float sl2, float &m_used, float &l,
+                                                   int j, uint32_t pv_done, const Ctl &ctl)
 {
-    if (j > 0) {  // streaming pass against the current max
-        Acc8 acc;
-        const float neg_m = MASK && m_used == -INFINITY ? 0.f : -m_used;
-        uint32_t ra[32], rb[32];
-        tmem_ld32(t_s, ra);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint32_t(&cur)[32] = (c & 1) ? rb : ra;
-            uint32_t(&nxt)[32] = (c & 1) ? ra : rb;
-            tmem_wait_ld_regs(cur);
-            if (c + 1 < 4) tmem_ld32(t_s + (c + 1) * 32, nxt);
-            hide_columns<MASK>(c, nv, cur);
-            if (c == 0 && pv_first) {
-                uint32_t pk[16];
-                exp_chunk(cur, sl2, neg_m, pk, acc);
-                if (!__all_sync(0xffffffffu, wait_bar(pv_first, (j - 1) & 1, ctl))) return false;
-                tc_fence_after();
-                store_chunk(pk, p_row, row, 0);
-            } else {
-                exp_store_chunk(cur, sl2, neg_m, p_row, row, c, acc);
-            }
-        }
-        const float lt = sum8(acc);
-        if (!__any_sync(0xffffffffu, lt > RESCALE_LIMIT || m_used == -INFINITY)) {
-            l += lt;
-            return true;
-        }
-    }
+    uint32_t ra[32], rb[32];  // the load of chunk c + 1 is in flight while chunk c is used
     float mx = -INFINITY;
+    tmem_ld32(t_s, ra);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-        uint32_t r[32];
-        tmem_ld32(t_s + c * 32, r);
-        tmem_wait_ld_regs(r);
-        hide_columns<MASK>(c, nv, r);
-        mx = fmaxf(mx, max32(r));
+        uint32_t(&cur)[32] = (c & 1) ? rb : ra;
+        uint32_t(&nxt)[32] = (c & 1) ? ra : rb;
+        tmem_wait_ld_regs(cur);
+        tmem_ld32(t_s + ((c + 1) & 3) * 32, nxt);  // after the last one: chunk 0 again, for its exponentials
+        hide_columns<MASK>(c, nv, cur);
+        mx = fmaxf(mx, max32(cur));
     }
     const float m_cand = mx * sl2;
-    const bool resc = m_cand > m_used;
-    const float m_new = resc ? m_cand : m_used;
-    const float neg_m = m_new == -INFINITY ? 0.f : -m_new;
-    const float alpha = m_used == -INFINITY ? 0.f : ex2_approx(m_used - m_new);
+    const bool grow = m_cand > m_used + 8.f;
+    if (__any_sync(0xffffffffu, grow)) {
+        const float m_new = grow ? m_cand : m_used;
+        const float alpha = !grow ? 1.f : m_used == -INFINITY ? 0.f : ex2_approx(m_used - m_new);
+        l *= alpha;
+        m_used = m_new;
+        if (j > 0) {
+            if (pv_done) {
+                if (!__all_sync(0xffffffffu, wait_bar(pv_done, (j - 1) & 1, ctl))) return false;
+                tc_fence_after();
+            }
+            tmem_wait_ld_regs(ra);  // chunk 0 has arrived before the loads below
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                tmem_ld32(t_o + c * 32, rb);
+                tmem_wait_ld_regs(rb);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) rb[i] = __float_as_uint(__uint_as_float(rb[i]) * alpha);
+                tmem_st32(t_o + c * 32, rb);
+            }
+        }
+    }
+    const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
     Acc8 acc;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-        uint32_t r[32];
-        tmem_ld32(t_s + c * 32, r);
-        tmem_wait_ld_regs(r);
-        hide_columns<MASK>(c, nv, r);
-        exp_store_chunk(r, sl2, neg_m, p_row, row, c, acc);
+        uint32_t(&cur)[32] = (c & 1) ? rb : ra;
+        uint32_t(&nxt)[32] = (c & 1) ? ra : rb;
+        tmem_wait_ld_regs(cur);
+        if (c < 3) tmem_ld32(t_s + (c + 1) * 32, nxt);
+        hide_columns<MASK>(c, nv, cur);
+        uint32_t pk[16];
+        exp_chunk(cur, sl2, neg_m, pk, acc);
+        tmem_st16(t_s + c * 16, pk);
     }
-    if (j > 0 && __any_sync(0xffffffffu, resc)) {
-        if (pv_done) {
-            if (!__all_sync(0xffffffffu, wait_bar(pv_done, (j - 1) & 1, ctl))) return false;
-            tc_fence_after();
-        }
-        const float by = resc ? alpha : 1.f;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(t_o + c * 32, o);
-            tmem_wait_ld_regs(o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
-            tmem_st32(t_o + c * 32, o);
-        }
-    }
-    l = l * (resc ? alpha : 1.f) + sum8(acc);
-    m_used = m_new;
+    l += sum8(acc);
     return true;
 }
 
@@ -712,10 +756,10 @@ template <int D>
 __device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *smem, uint32_t sbase, uint32_t tmem, int x,
                                    int key0, int n_tiles, bool one_tile, const Ctl &ctl)
 {
-    using C = Cfg<D>;
+    using C = CCfg<D>;
     constexpr int LR = D / 8;     // lanes per 16-byte-pieced row
     constexpr int RPI = 32 / LR;  // rows per access of a warp
-    const Bars<D> bar{sbase + C::SMEM_BAR};
+    const CBars<D> bar{sbase + C::SMEM_BAR};
     volatile int32_t *epi_ok = reinterpret_cast<volatile int32_t *>(smem + C::SMEM_BAR + 160) + 4 * x;
     const int row = threadIdx.x & 127, lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
     const int tile_row0 = u.row0 + x * BM;
@@ -748,24 +792,20 @@ __device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *s
         const int xb = one_tile ? (j & 1) : x;
         const uint32_t par = one_tile ? (uint32_t)(j >> 1) & 1 : (uint32_t)j & 1;
         const uint32_t t_s = lane_base + tcol_s(xb);
-        const uint32_t p_row = sbase + C::SMEM_P + xb * C::P_BYTES + row * 128;
         if (!__all_sync(0xffffffffu, wait_bar(bar.s_full(xb), par, ctl))) {
             alive = false;
             break;
         }
         tc_fence_after();
         const uint32_t pvw = one_tile ? bar.pv_done() : 0u;
-        const uint32_t pvf = (!one_tile && j > 0) ? bar.pv_x(x) : 0u;
         const bool whole = lim_warp >= (j + 1) * BN;
-        const bool ok = whole ? chunk_softmax_tile<D, false>(t_s, p_row, row, t_o, BN, a.scale_log2, m_used, l, j, pvw, pvf, ctl)
-                              : chunk_softmax_tile<D, true>(t_s, p_row, row, t_o, lim - j * BN, a.scale_log2, m_used, l, j,
-                                                            pvw, pvf, ctl);
+        const bool ok = whole ? chunk_softmax_tile<D, false>(t_s, t_o, BN, a.scale_log2, m_used, l, j, pvw, ctl)
+                              : chunk_softmax_tile<D, true>(t_s, t_o, lim - j * BN, a.scale_log2, m_used, l, j, pvw, ctl);
         if (!ok) {
             alive = false;
             break;
         }
         tmem_wait_st();
-        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0 && !((a.debug_flags & SFA_DEBUG_STALL_SOFTMAX) && j == 0)) mbar_arrive(bar.p_full(xb));
@@ -828,7 +868,7 @@ __device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *s
 template <int D>
 __global__ void __launch_bounds__(CT_THREADS, 1) tile_attn_kernel(const __grid_constant__ ChunkArgs a)
 {
-    using C = Cfg<D>;
+    using C = CCfg<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -849,10 +889,10 @@ __global__ void __launch_bounds__(CT_THREADS, 1) tile_attn_kernel(const __grid_c
     const bool has_b = u.row0 + BM < u.n_rows;
 
     if (threadIdx.x == 0) {
-        const Bars<D> bar{sbase + C::SMEM_BAR};
-        for (int i = 0; i < Bars<D>::COUNT; ++i) mbar_init(sbase + C::SMEM_BAR + 8 * i, 1);
-        for (int s = 0; s < C::NSK; ++s) mbar_init(bar.k_full(s), CT_CONV_WARPS);
-        for (int s = 0; s < C::NSV; ++s) mbar_init(bar.v_full(s), CT_CONV_WARPS);
+        const CBars<D> bar{sbase + C::SMEM_BAR};
+        for (int i = 0; i < CBars<D>::COUNT; ++i) mbar_init(sbase + C::SMEM_BAR + 8 * i, 1);
+        for (int s = 0; s < C::NSK; ++s) mbar_init(bar.k_full(s), CT_K_WARPS);
+        for (int s = 0; s < C::NSV; ++s) mbar_init(bar.v_full(s), CT_V_WARPS);
         mbar_init(bar.q_full(), has_b ? CT_SOFTMAX_WARPS : CT_SOFTMAX_WARPS / 2);
         mbar_init(bar.p_full(0), BM / 32);
         mbar_init(bar.p_full(1), BM / 32);
@@ -875,13 +915,17 @@ __global__ void __launch_bounds__(CT_THREADS, 1) tile_attn_kernel(const __grid_c
 
     if (warp == CT_MMA_WARP) {
         if (n_tiles > 0) {
-            if (has_b) chunk_mma_pair<D>(sbase, tmem, n_tiles, ctl);
-            else chunk_mma_single<D>(sbase, tmem, n_tiles, ctl);
+            if (has_b) chunk_mma<D, true>(sbase, tmem, n_tiles, ctl);
+            else chunk_mma<D, false>(sbase, tmem, n_tiles, ctl);
         }
-    } else if (warp >= CT_CONV_WARP) {
-        if (n_tiles > 0) convert_role<D>(a, u, sbase, t0 * BN, seen, n_tiles, ctl);
-    } else if (!skipped && (warp < 4 || has_b)) {
-        chunk_softmax_role<D>(a, u, smem, sbase, tmem, warp >> 2, t0 * BN, n_tiles, !has_b, ctl);
+    } else if (warp >= CT_K_WARP) {
+        if (n_tiles > 0) {
+            if (warp < CT_V_WARP) convert_role<D, true>(a, u, sbase, t0 * BN, seen, n_tiles, ctl);
+            else convert_role<D, false>(a, u, sbase, t0 * BN, seen, n_tiles, ctl);
+        }
+    } else {
+        if (!skipped && (warp < 4 || has_b))
+            chunk_softmax_role<D>(a, u, smem, sbase, tmem, warp >> 2, t0 * BN, n_tiles, !has_b, ctl);
     }
 
     tc_fence_before();
@@ -1001,10 +1045,10 @@ Plan plan_of(const sfa_cache_attn_desc *d, const sfa_cache *c)
 template <int D>
 sfa_status launch_tiles(const ChunkArgs &a, unsigned grid, cudaStream_t s)
 {
-    if (cudaFuncSetAttribute(tile_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM_BYTES) !=
+    if (cudaFuncSetAttribute(tile_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, CCfg<D>::SMEM_BYTES) !=
         cudaSuccess)
         return SFA_ERR_CUDA;
-    tile_attn_kernel<D><<<grid, CT_THREADS, Cfg<D>::SMEM_BYTES, s>>>(a);
+    tile_attn_kernel<D><<<grid, CT_THREADS, CCfg<D>::SMEM_BYTES, s>>>(a);
     return launch_status();
 }
 
