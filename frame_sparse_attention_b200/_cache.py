@@ -9,46 +9,25 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import NamedTuple
 
 import torch
 
-from ._lib import _check, _require, load
+from ._lib import SfaError, _check, _require, load
 
 CACHE_BLOCK = 32  # elements of a cached row that share a scale
 ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
 ROPE_MAX_AXES = 4
 
-_i32, _i64, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
+# The descriptors of include/sfa.h as native structs (field by field, C's padding written out)
+_CACHE = struct.Struct("@4i5Pi4x2q")        # sfa_cache
+_ROPE = struct.Struct("@2P2q6if4x")         # sfa_rope: inv_freq, positions, strides, layout, n_axes, axis_pairs, scale
+_ROWS = struct.Struct("@5if18q2q")          # sfa_rows_desc: sizes, eps, q, k, v, q_out, k_out, v_out and start strides
+_ATTN = struct.Struct("@5if2i6q2q2I")       # sfa_cache_attn_desc
 
-
-class CacheDesc(ctypes.Structure):
-    """sfa_cache."""
-    _fields_ = [("n_pages", _i32), ("heads", _i32), ("page_len", _i32), ("d", _i32), ("k", _vp), ("v", _vp),
-                ("k_scale", _vp), ("v_scale", _vp), ("table", _vp), ("table_len", _i32),
-                ("table_stride_b", _i64), ("table_stride_h", _i64)]
-
-
-class RopeDesc(ctypes.Structure):
-    """sfa_rope."""
-    _fields_ = [("inv_freq", _vp), ("positions", _vp), ("pos_stride_b", _i64), ("pos_stride_t", _i64),
-                ("layout", _i32), ("n_axes", _i32), ("axis_pairs", _i32 * ROPE_MAX_AXES), ("scale", _f32)]
-
-
-class RowsDesc(ctypes.Structure):
-    """sfa_rows_desc (each stride array as its three entries)."""
-    _fields_ = [("B", _i32), ("H", _i32), ("H_kv", _i32), ("L", _i32), ("d", _i32), ("eps", _f32)] + \
-               [(f"{t}_stride{i}", _i64) for t in ("q", "k", "v", "q_out", "k_out", "v_out") for i in range(3)] + \
-               [("start_stride_b", _i64), ("start_stride_h", _i64)]
-
-
-class CacheAttnDesc(ctypes.Structure):
-    """sfa_cache_attn_desc."""
-    _fields_ = [("B", _i32), ("H", _i32), ("H_kv", _i32), ("Lq", _i32), ("d", _i32), ("scale", _f32), ("causal", _i32),
-                ("max_kv", _i32)] + \
-               [(f"{t}_stride{i}", _i64) for t in ("q", "o") for i in range(3)] + \
-               [("len_stride_b", _i64), ("len_stride_h", _i64), ("timeout_us", ctypes.c_uint32),
-                ("debug_flags", ctypes.c_uint32)]
+_BF16, _I32, _F32, _F64 = torch.bfloat16, torch.int32, torch.float32, torch.float64
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
 
 class RopeTable(NamedTuple):
@@ -116,107 +95,121 @@ def rope_table(axis_dims, theta: float = 10000.0, scaling: str = "none", factor:
 
 
 # ---------------------------------------------------------------- marshalling
-def _launch(device, fn, args, stream, what):
-    """fn(*args, stream) with ``device`` current."""
-    if device.type != "cuda":
+# These calls are a few microseconds of GPU time at a single token, so the checks below are
+# written for few interpreter steps.
+def _current_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+
+
+def _launch(dev, fn, args, stream, what):
+    """fn(*args, stream) with device ``dev`` current."""
+    if dev < 0:
         raise ValueError(f"{what}: expected CUDA tensors")
-    index = device.index
-    if index == torch.cuda.current_device():
-        if stream is None:
-            stream = torch.cuda.current_stream().cuda_stream
-        elif not isinstance(stream, int):
-            stream = stream.cuda_stream
-        status = fn(*args, stream)
+    if stream is not None and not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(dev) if stream is None else stream)
     else:
-        with torch.cuda.device(index):
-            if stream is None:
-                stream = torch.cuda.current_stream().cuda_stream
-            elif not isinstance(stream, int):
-                stream = stream.cuda_stream
-            status = fn(*args, stream)
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(dev) if stream is None else stream)
     if status:
-        _check(status, what)
+        raise SfaError(status, what)
 
 
-def _rows(name, t, device, shape=None):
-    if t.dtype != torch.bfloat16 or t.device != device or t.dim() != 4 or t.stride(3) != 1:
-        raise ValueError(f"{name} must be a bf16 tensor [B, H, L, d] on {device} with d contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, has {tuple(t.shape)}")
+def _rows(name, t, dev, shape):
+    """(strides, address) of a bf16 tensor of this shape."""
+    if t.dtype is not _BF16 or t.get_device() != dev or t.shape != shape:
+        raise ValueError(f"{name} must be a bf16 tensor {tuple(shape)} on device {dev}: {t.dtype} {tuple(t.shape)}")
+    st = t.stride()
+    if st[3] != 1:
+        raise ValueError(f"{name} must have d contiguous")
+    return st[:3], t.data_ptr()
 
 
-def _ints(name, t, device, shapes):
-    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) not in shapes:
-        raise ValueError(f"{name} must be an int32 tensor on {device} of shape {' or '.join(map(str, shapes))}")
+def _shape4(name, t):
+    s = t.shape
+    if len(s) != 4:
+        raise ValueError(f"{name} must be [B, H, L, d]")
+    return s
 
 
-def _check_status(dev_status, device):
-    if dev_status is not None:
-        _require(dev_status.dtype == torch.int32 and dev_status.device == device and dev_status.numel() >= 1,
-                 f"dev_status must be an int32 tensor on {device}")
-        return dev_status.data_ptr()
-    return None
+def _per_head(name, t, dev, B, H_kv):
+    """(batch stride, head stride) of an int32 tensor [B], [B, 1] or [B, H_kv]."""
+    s = t.shape
+    if t.dtype is not _I32 or t.get_device() != dev or len(s) not in (1, 2) or s[0] != B or \
+            (len(s) == 2 and s[1] != H_kv and s[1] != 1):
+        raise ValueError(f"{name} must be an int32 tensor [{B}] or [{B}, {H_kv}] on device {dev}")
+    st = t.stride()
+    return (st[0], st[1]) if len(s) == 2 and s[1] > 1 else (st[0], 0)
 
 
-def _per_head(name, t, device, B, H_kv):
-    """(batch stride, head stride) of an int32 tensor [B] or [B, H_kv]."""
-    _ints(name, t, device, ((B,), (B, H_kv), (B, 1)))
-    return t.stride(0), (t.stride(1) if t.dim() == 2 and t.shape[1] > 1 else 0)
-
-
-def _lens(lens, device, B):
-    if lens is None:
+def _lens(name, t, dev, B):
+    if t is None:
         return None
-    _ints("lens", lens, device, ((B,),))
-    _require(lens.is_contiguous(), "expected lens.is_contiguous()")
-    return lens.data_ptr()
+    if t.dtype is not _I32 or t.get_device() != dev or t.shape != (B,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor [{B}] on device {dev}")
+    return t.data_ptr()
 
 
-def _weight(name, w, device, d):
+def _status(t, dev):
+    if t is None:
+        return None
+    if t.dtype is not _I32 or t.get_device() != dev or t.numel() < 1:
+        raise ValueError(f"dev_status must be an int32 tensor on device {dev}")
+    return t.data_ptr()
+
+
+def _weight(name, w, dev, d):
     if w is None:
         return None
-    if w.dtype != torch.float32 or w.device != device or tuple(w.shape) != (d,) or not w.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous fp32 tensor [{d}] on {device}")
+    if w.dtype is not _F32 or w.get_device() != dev or w.shape != (d,) or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous fp32 tensor [{d}] on device {dev}")
     return w.data_ptr()
 
 
-def _cache_desc(cache, table, device, B, H_kv, d):
-    k, ks, v, vs = cache.k, cache.k_scale, cache.v, cache.v_scale
-    shape = tuple(k.shape)
-    _require(len(shape) == 4 and shape[3] == d, f"expected cache codes [n_pages, heads, page_len, {d}]")
-    s_shape = shape[:3] + (d // CACHE_BLOCK,)
-    for name, t, want, dtype in (("k", k, shape, torch.float8_e4m3fn), ("v", v, shape, torch.float8_e4m3fn),
-                                 ("k_scale", ks, s_shape, torch.float8_e8m0fnu),
-                                 ("v_scale", vs, s_shape, torch.float8_e8m0fnu)):
-        if t.dtype != dtype or t.device != device or tuple(t.shape) != want or not t.is_contiguous():
-            raise ValueError(f"cache.{name} must be a contiguous {dtype} tensor {want} on {device}")
-    _require(table.dtype == torch.int32 and table.device == device and table.dim() in (2, 3) and table.stride(-1) == 1,
-             f"table must be an int32 tensor [B, N] or [B, H_kv, N] on {device}")
-    rows = table.shape[1] if table.dim() == 3 else 1
-    _require(table.shape[0] == B and rows in (1, H_kv), f"expected table [{B}, {H_kv} or 1, N]")
-    return CacheDesc(shape[0], shape[1], shape[2], d, k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(),
-                     table.data_ptr(), table.shape[-1], table.stride(0), table.stride(1) if rows > 1 else 0)
+def _cache_desc(cache, table, dev, B, H_kv, d):
+    k, ks, v, vs = cache
+    shape = k.shape
+    if len(shape) != 4 or shape[3] != d:
+        raise ValueError(f"expected cache codes [n_pages, heads, page_len, {d}], have {tuple(shape)}")
+    scales = (*shape[:3], d // CACHE_BLOCK)
+    if k.dtype is not _E4M3 or v.dtype is not _E4M3 or ks.dtype is not _E8M0 or vs.dtype is not _E8M0 or \
+            v.shape != shape or ks.shape != scales or vs.shape != scales:
+        raise ValueError(f"expected a cache of float8_e4m3fn codes {tuple(shape)} and float8_e8m0fnu scales {scales}")
+    if k.get_device() != dev or v.get_device() != dev or ks.get_device() != dev or vs.get_device() != dev or \
+            not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+        raise ValueError(f"expected a contiguous cache on device {dev}")
+    ts, st = table.shape, table.stride()
+    if table.dtype is not _I32 or table.get_device() != dev or len(ts) not in (2, 3) or ts[0] != B or \
+            (ts[-1] > 1 and st[-1] != 1) or (len(ts) == 3 and ts[1] != 1 and ts[1] != H_kv):
+        raise ValueError(f"table must be an int32 tensor [{B}, N] or [{B}, {H_kv}, N] on device {dev}, rows contiguous")
+    return _CACHE.pack(*shape, k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), table.data_ptr(), ts[-1],
+                       st[0], st[1] if len(ts) == 3 and ts[1] > 1 else 0)
 
 
-def _rope_desc(rope, positions, layout, device, B, L):
-    """A pointer to the sfa_rope of this call, or None."""
+def _rope_desc(rope, positions, layout, dev, B, L):
+    """The sfa_rope of this call, or None."""
     if rope is None:
         return None
-    f, pairs = rope.inv_freq, rope.axis_pairs
-    if f.dtype != torch.float64 or f.device != device or not f.is_contiguous() or f.numel() != sum(pairs):
-        raise ValueError(f"rope.inv_freq must be a contiguous float64 tensor [{sum(pairs)}] on {device}")
-    _require(layout in ROPE_LAYOUTS, "expected layout 'interleaved' or 'half'")
+    f, pairs, scale = rope
     n = len(pairs)
-    _require(0 < n <= ROPE_MAX_AXES, "expected 1 to 4 position axes")
-    _require(positions is not None, "rope needs positions")
-    _ints("positions", positions, device, ((B, L, n), (1, L, n), (L, n)))
-    _require(n == 1 or positions.stride(-1) == 1, "expected positions with the axes contiguous")
-    sb = positions.stride(0) if positions.dim() == 3 and positions.shape[0] == B else 0
-    r = RopeDesc(f.data_ptr(), positions.data_ptr(), sb, positions.stride(-2), ROPE_LAYOUTS[layout], n)
-    r.scale = rope.scale
-    for i, p in enumerate(pairs):
-        r.axis_pairs[i] = p
-    return ctypes.byref(r)
+    if not 0 < n <= ROPE_MAX_AXES:
+        raise ValueError(f"expected 1 to {ROPE_MAX_AXES} position axes")
+    if f.dtype is not _F64 or f.get_device() != dev or f.shape != (sum(pairs),) or not f.is_contiguous():
+        raise ValueError(f"rope.inv_freq must be a contiguous float64 tensor [{sum(pairs)}] on device {dev}")
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError("expected layout 'interleaved' or 'half'")
+    if positions is None:
+        raise ValueError("rope needs positions")
+    s, st = positions.shape, positions.stride()
+    if positions.dtype is not _I32 or positions.get_device() != dev or len(s) not in (2, 3) or s[-1] != n or \
+            s[-2] != L or (len(s) == 3 and s[0] != B and s[0] != 1) or (n > 1 and st[-1] != 1):
+        raise ValueError(f"positions must be an int32 tensor [{B}, {L}, {n}] or [{L}, {n}] on device {dev}")
+    return _ROPE.pack(f.data_ptr(), positions.data_ptr(), st[0] if len(s) == 3 and s[0] == B else 0, st[-2],
+                      ROPE_LAYOUTS[layout], n, *pairs, *(0,) * (ROPE_MAX_AXES - n), scale)
 
 
 _NO = (0, 0, 0)
@@ -230,45 +223,47 @@ def qk_norm_rope(q, k=None, rope: RopeTable | None = None, positions=None, q_wei
     (ones); eps None: no norm.  rope None: no rotation, else positions int32 [B, L, axes]
     (or [L, axes], shared by the batch).  Returns (q_out, k_out), bf16, None where there was no
     input; an output may be its input (in place)."""
-    t = q if q is not None else k
-    _require(t is not None, "qk_norm_rope needs q or k")
-    device = t.device
-    _require(t.dim() == 4, "expected tensors [B, H, L, d]")
-    B, _, L, d = t.shape
-    H, H_kv, sq, so, sk, sko = 0, 0, _NO, _NO, _NO, _NO
+    t = k if q is None else q
+    if t is None:
+        raise ValueError("qk_norm_rope needs q or k")
+    dev = t.get_device()
+    B, _, L, d = _shape4("q and k", t)
+    H = H_kv = 0
+    sq = so = sk = sko = _NO
     qp = qop = kp = kop = None
     if q is not None:
-        _rows("q", q, device)
+        shape = q.shape
+        H = shape[1]
+        sq, qp = _rows("q", q, dev, shape)
         q_out = torch.empty_like(q) if q_out is None else q_out
-        _rows("q_out", q_out, device, q.shape)
-        H, sq, so, qp, qop = q.shape[1], q.stride(), q_out.stride(), q.data_ptr(), q_out.data_ptr()
+        so, qop = _rows("q_out", q_out, dev, shape)
     if k is not None:
-        _rows("k", k, device, (B, k.shape[1], L, d))
+        H_kv = _shape4("k", k)[1]
+        shape = (B, H_kv, L, d)
+        sk, kp = _rows("k", k, dev, shape)
         k_out = torch.empty_like(k) if k_out is None else k_out
-        _rows("k_out", k_out, device, k.shape)
-        H_kv, sk, sko, kp, kop = k.shape[1], k.stride(), k_out.stride(), k.data_ptr(), k_out.data_ptr()
-    desc = RowsDesc(B, H, H_kv, L, d, -1.0 if eps is None else eps, *sq[:3], *sk[:3], *_NO, *so[:3], *sko[:3])
-    _launch(device, load().sfa_qk_norm_rope,
-            (ctypes.byref(desc), _rope_desc(rope, positions, layout, device, B, L), qp, kp,
-             _weight("q_weight", q_weight, device, d), _weight("k_weight", k_weight, device, d), qop, kop),
-            stream, "sfa_qk_norm_rope")
-    return q_out if q is not None else None, k_out if k is not None else None
+        sko, kop = _rows("k_out", k_out, dev, shape)
+    desc = _ROWS.pack(B, H, H_kv, L, d, -1.0 if eps is None else eps, *sq, *sk, *_NO, *so, *sko, *_NO, 0, 0)
+    _launch(dev, load().sfa_qk_norm_rope,
+            (desc, _rope_desc(rope, positions, layout, dev, B, L), qp, kp, _weight("q_weight", q_weight, dev, d),
+             _weight("k_weight", k_weight, dev, d), qop, kop), stream, "sfa_qk_norm_rope")
+    return None if q is None else q_out, None if k is None else k_out
 
 
 def cache_write(cache: FrameCache, k, v, table, start, lens=None, dev_status=None, stream=None):
     """Write new keys and values bf16 [B, H_kv, L, d] into the cache: token i of (b, h) becomes
     logical token start[b][h] + i.  table int32 [B, N] or [B, H_kv, N] of page numbers, start
     int32 [B] or [B, H_kv], lens int32 [B] (rows from there on are padding) or None."""
-    device = k.device
-    _rows("k", k, device)
-    _rows("v", v, device, k.shape)
-    B, H_kv, L, d = k.shape
-    cd = _cache_desc(cache, table, device, B, H_kv, d)
-    desc = RowsDesc(B, 0, H_kv, L, d, -1.0, *_NO, *k.stride()[:3], *v.stride()[:3], *_NO, *_NO, *_NO,
-                    *_per_head("start", start, device, B, H_kv))
-    _launch(device, load().sfa_cache_write,
-            (ctypes.byref(desc), ctypes.byref(cd), k.data_ptr(), v.data_ptr(), start.data_ptr(),
-             _lens(lens, device, B), _check_status(dev_status, device)), stream, "sfa_cache_write")
+    dev = k.get_device()
+    shape = _shape4("k", k)
+    sk, kp = _rows("k", k, dev, shape)
+    sv, vp = _rows("v", v, dev, shape)
+    B, H_kv, L, d = shape
+    cd = _cache_desc(cache, table, dev, B, H_kv, d)
+    desc = _ROWS.pack(B, 0, H_kv, L, d, -1.0, *_NO, *sk, *sv, *_NO, *_NO, *_NO, *_per_head("start", start, dev, B, H_kv))
+    _launch(dev, load().sfa_cache_write,
+            (desc, cd, kp, vp, start.data_ptr(), _lens("lens", lens, dev, B), _status(dev_status, dev)), stream,
+            "sfa_cache_write")
 
 
 def cache_append(cache: FrameCache, q, k, v, table, start, lens=None, rope: RopeTable | None = None, positions=None,
@@ -277,22 +272,23 @@ def cache_append(cache: FrameCache, q, k, v, table, start, lens=None, rope: Rope
     """qk_norm_rope of q and k, and cache_write of those keys and v, in one pass (the bf16 keys
     are not written).  Arguments as theirs; returns q_out.  Padding rows of q_out (from lens[b]
     on) are left as they are."""
-    device = q.device
-    _rows("q", q, device)
-    B, H, L, d = q.shape
-    _rows("k", k, device, (B, k.shape[1], L, d))
-    _rows("v", v, device, k.shape)
-    H_kv = k.shape[1]
+    dev = q.get_device()
+    shape = _shape4("q", q)
+    B, H, L, d = shape
+    H_kv = _shape4("k", k)[1]
+    kv_shape = (B, H_kv, L, d)
+    sq, qp = _rows("q", q, dev, shape)
+    sk, kp = _rows("k", k, dev, kv_shape)
+    sv, vp = _rows("v", v, dev, kv_shape)
     q_out = torch.empty_like(q) if q_out is None else q_out
-    _rows("q_out", q_out, device, q.shape)
-    cd = _cache_desc(cache, table, device, B, H_kv, d)
-    desc = RowsDesc(B, H, H_kv, L, d, -1.0 if eps is None else eps, *q.stride()[:3], *k.stride()[:3],
-                    *v.stride()[:3], *q_out.stride()[:3], *_NO, *_NO, *_per_head("start", start, device, B, H_kv))
-    _launch(device, load().sfa_cache_append,
-            (ctypes.byref(desc), _rope_desc(rope, positions, layout, device, B, L), ctypes.byref(cd), q.data_ptr(),
-             k.data_ptr(), v.data_ptr(), _weight("q_weight", q_weight, device, d),
-             _weight("k_weight", k_weight, device, d), q_out.data_ptr(), start.data_ptr(), _lens(lens, device, B),
-             _check_status(dev_status, device)), stream, "sfa_cache_append")
+    so, qop = _rows("q_out", q_out, dev, shape)
+    cd = _cache_desc(cache, table, dev, B, H_kv, d)
+    desc = _ROWS.pack(B, H, H_kv, L, d, -1.0 if eps is None else eps, *sq, *sk, *sv, *so, *_NO, *_NO,
+                      *_per_head("start", start, dev, B, H_kv))
+    _launch(dev, load().sfa_cache_append,
+            (desc, _rope_desc(rope, positions, layout, dev, B, L), cd, qp, kp, vp,
+             _weight("q_weight", q_weight, dev, d), _weight("k_weight", k_weight, dev, d), qop, start.data_ptr(),
+             _lens("lens", lens, dev, B), _status(dev_status, dev)), stream, "sfa_cache_append")
     return q_out
 
 
@@ -301,44 +297,45 @@ def cache_read(cache: FrameCache, table, start, L: int, lens=None, k_out=None, v
     """Logical tokens start[b][h] + i, i < min(L, lens[b]), of every (b, h) back as bf16
     [B, H_kv, L, d]: (k_out, v_out).  Other rows are left as they are (zero where the outputs
     are allocated here).  H_kv: key heads, where neither the pool nor the table says so."""
-    device = cache.k.device
-    _require(cache.k.dim() == 4 and table.dim() in (2, 3), "expected cache codes [n_pages, heads, page_len, d]")
-    B, d = table.shape[0], cache.k.shape[3]
+    pool, t = _shape4("cache.k", cache.k), table.shape
+    dev, B, d = cache.k.get_device(), t[0], pool[3]
     if H_kv is None:
-        H_kv = k_out.shape[1] if k_out is not None else max(cache.k.shape[1], table.shape[1] if table.dim() == 3 else 1)
+        H_kv = _shape4("k_out", k_out)[1] if k_out is not None else max(pool[1], t[1] if len(t) == 3 else 1)
     shape = (B, H_kv, int(L), d)
-    k_out = torch.zeros(shape, dtype=torch.bfloat16, device=device) if k_out is None else k_out
-    v_out = torch.zeros(shape, dtype=torch.bfloat16, device=device) if v_out is None else v_out
-    _rows("k_out", k_out, device, shape)
-    _rows("v_out", v_out, device, shape)
-    cd = _cache_desc(cache, table, device, B, H_kv, d)
-    desc = RowsDesc(B, 0, H_kv, int(L), d, -1.0, *_NO, *_NO, *_NO, *_NO, *k_out.stride()[:3], *v_out.stride()[:3],
-                    *_per_head("start", start, device, B, H_kv))
-    _launch(device, load().sfa_cache_read,
-            (ctypes.byref(desc), ctypes.byref(cd), start.data_ptr(), _lens(lens, device, B), k_out.data_ptr(),
-             v_out.data_ptr(), _check_status(dev_status, device)), stream, "sfa_cache_read")
+    if k_out is None:
+        k_out = torch.zeros(shape, dtype=_BF16, device=cache.k.device)
+    if v_out is None:
+        v_out = torch.zeros(shape, dtype=_BF16, device=cache.k.device)
+    sk, kp = _rows("k_out", k_out, dev, shape)
+    sv, vp = _rows("v_out", v_out, dev, shape)
+    cd = _cache_desc(cache, table, dev, B, H_kv, d)
+    desc = _ROWS.pack(B, 0, H_kv, shape[2], d, -1.0, *_NO, *_NO, *_NO, *_NO, *sk, *sv,
+                      *_per_head("start", start, dev, B, H_kv))
+    _launch(dev, load().sfa_cache_read,
+            (desc, cd, start.data_ptr(), _lens("lens", lens, dev, B), kp, vp, _status(dev_status, dev)), stream,
+            "sfa_cache_read")
     return k_out, v_out
 
 
-def _attn(q, cache, table, kv_lens, causal, max_kv, scale, out, H_kv, timeout_us=0, debug_flags=0):
-    device = q.device
-    B, H, Lq, d = q.shape
-    if H_kv is None:
-        H_kv = max(cache.k.shape[1], table.shape[1] if table.dim() == 3 else 1,
-                   kv_lens.shape[1] if kv_lens.dim() == 2 else 1)
-    cd = _cache_desc(cache, table, device, B, H_kv, d)
-    desc = CacheAttnDesc(B, H, H_kv, Lq, d, 1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0, max_kv,
-                         *q.stride()[:3], *out.stride()[:3], *_per_head("kv_lens", kv_lens, device, B, H_kv),
-                         timeout_us, debug_flags)
-    return desc, cd
+def _key_heads(cache, table, kv_lens):
+    """Key heads as the pool, the table or the lengths have them."""
+    n, t = cache.k.shape[1], table.shape
+    if n == 1 and len(t) == 3:
+        n = t[1]
+    if n == 1 and kv_lens.dim() == 2:
+        n = kv_lens.shape[1]
+    return n
 
 
 def forward_cache_workspace_bytes(q, cache: FrameCache, table, kv_lens, max_kv: int = 0, H_kv: int | None = None) -> int:
     """Device workspace bytes of forward_cache for these shapes."""
-    desc, cd = _attn(q, cache, table, kv_lens, False, max_kv, None, q, H_kv)
+    B, H, Lq, d = _shape4("q", q)
+    if H_kv is None:
+        H_kv = _key_heads(cache, table, kv_lens)
+    cd = _cache_desc(cache, table, q.get_device(), B, H_kv, d)
+    desc = _ATTN.pack(B, H, H_kv, Lq, d, 1.0, 0, max_kv, *_NO, *_NO, 0, 0, 0, 0)
     out = ctypes.c_size_t(0)
-    _check(load().sfa_forward_cache_workspace(ctypes.byref(desc), ctypes.byref(cd), ctypes.byref(out)),
-           "sfa_forward_cache_workspace")
+    _check(load().sfa_forward_cache_workspace(desc, cd, ctypes.byref(out)), "sfa_forward_cache_workspace")
     return out.value
 
 
@@ -354,28 +351,31 @@ def forward_cache(q, cache: FrameCache, table, kv_lens, causal: bool = False, q_
     tensor of forward_cache_workspace_bytes (allocated here when not given).  H_kv: key heads,
     where neither the pool, the table nor kv_lens says so.  Rows that see no key give O = 0,
     LSE = -inf, so the result merges with other branches by lse_merge."""
-    device = q.device
-    _rows("q", q, device)
-    B, H, Lq, d = q.shape
+    dev = q.get_device()
+    shape = _shape4("q", q)
+    sq, qp = _rows("q", q, dev, shape)
     out = torch.empty_like(q) if out is None else out
-    _rows("out", out, device, q.shape)
+    so, op = _rows("out", out, dev, shape)
+    B, H, Lq, d = shape
     if lse is None:
-        lse = torch.empty((B, H, Lq), dtype=torch.float32, device=device)
-    elif lse.dtype != torch.float32 or lse.device != device or tuple(lse.shape) != (B, H, Lq) or not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous fp32 tensor {(B, H, Lq)} on {device}")
-    desc, cd = _attn(q, cache, table, kv_lens, causal, max_kv, scale, out, H_kv, timeout_us, debug_flags)
+        lse = torch.empty(shape[:3], dtype=_F32, device=q.device)
+    elif lse.dtype is not _F32 or lse.get_device() != dev or lse.shape != shape[:3] or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous fp32 tensor {tuple(shape[:3])} on device {dev}")
+    if H_kv is None:
+        H_kv = _key_heads(cache, table, kv_lens)
+    cd = _cache_desc(cache, table, dev, B, H_kv, d)
+    desc = _ATTN.pack(B, H, H_kv, Lq, d, 1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0, max_kv,
+                      *sq, *so, *_per_head("kv_lens", kv_lens, dev, B, H_kv), timeout_us, debug_flags)
     lib = load()
     if workspace is None:
         need = ctypes.c_size_t(0)
-        _check(lib.sfa_forward_cache_workspace(ctypes.byref(desc), ctypes.byref(cd), ctypes.byref(need)),
-               "sfa_forward_cache_workspace")
+        _check(lib.sfa_forward_cache_workspace(desc, cd, ctypes.byref(need)), "sfa_forward_cache_workspace")
         if need.value:
-            workspace = torch.empty(need.value, dtype=torch.uint8, device=device)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+            workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on device {dev}")
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _launch(device, lib.sfa_forward_cache,
-            (ctypes.byref(desc), ctypes.byref(cd), q.data_ptr(), kv_lens.data_ptr(), _lens(q_lens, device, B),
-             out.data_ptr(), lse.data_ptr(), ws, ws_bytes, _check_status(dev_status, device)), stream,
-            "sfa_forward_cache")
+    _launch(dev, lib.sfa_forward_cache,
+            (desc, cd, qp, kv_lens.data_ptr(), _lens("q_lens", q_lens, dev, B), op, lse.data_ptr(), ws, ws_bytes,
+             _status(dev_status, dev)), stream, "sfa_forward_cache")
     return out, lse

@@ -21,15 +21,48 @@ def sfa():
 GOOD = 1 << 20  # an aligned address that no accepted call would survive using
 
 
-def _structs():
+_i32, _i64, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
+
+
+class CacheDesc(ctypes.Structure):  # sfa_cache
+    _fields_ = [("n_pages", _i32), ("heads", _i32), ("page_len", _i32), ("d", _i32), ("k", _vp), ("v", _vp),
+                ("k_scale", _vp), ("v_scale", _vp), ("table", _vp), ("table_len", _i32),
+                ("table_stride_b", _i64), ("table_stride_h", _i64)]
+
+
+class RopeDesc(ctypes.Structure):  # sfa_rope
+    _fields_ = [("inv_freq", _vp), ("positions", _vp), ("pos_stride_b", _i64), ("pos_stride_t", _i64),
+                ("layout", _i32), ("n_axes", _i32), ("axis_pairs", _i32 * 4), ("scale", _f32)]
+
+
+class RowsDesc(ctypes.Structure):  # sfa_rows_desc
+    _fields_ = [("B", _i32), ("H", _i32), ("H_kv", _i32), ("L", _i32), ("d", _i32), ("eps", _f32)] + \
+               [(f"{t}_stride{i}", _i64) for t in ("q", "k", "v", "q_out", "k_out", "v_out") for i in range(3)] + \
+               [("start_stride_b", _i64), ("start_stride_h", _i64)]
+
+
+class CacheAttnDesc(ctypes.Structure):  # sfa_cache_attn_desc
+    _fields_ = [("B", _i32), ("H", _i32), ("H_kv", _i32), ("Lq", _i32), ("d", _i32), ("scale", _f32), ("causal", _i32),
+                ("max_kv", _i32)] + \
+               [(f"{t}_stride{i}", _i64) for t in ("q", "o") for i in range(3)] + \
+               [("len_stride_b", _i64), ("len_stride_h", _i64), ("timeout_us", ctypes.c_uint32),
+                ("debug_flags", ctypes.c_uint32)]
+
+
+def test_the_bindings_structs_have_cs_sizes(sfa):
     from frame_sparse_attention_b200 import _cache as c
-    rows = c.RowsDesc(2, 4, 2, 8, 64, 1e-6)
+    for packed, struct in ((c._CACHE, CacheDesc), (c._ROPE, RopeDesc), (c._ROWS, RowsDesc), (c._ATTN, CacheAttnDesc)):
+        assert packed.size == ctypes.sizeof(struct)
+
+
+def _structs():
+    rows = RowsDesc(2, 4, 2, 8, 64, 1e-6)
     for t, heads in (("q", 4), ("k", 2), ("v", 2), ("q_out", 4), ("k_out", 2), ("v_out", 2)):
         for i, s in enumerate((heads * 8 * 64, 8 * 64, 64)):
             setattr(rows, f"{t}_stride{i}", s)
     rows.start_stride_b = 1
-    cache = c.CacheDesc(4, 2, 16, 64, GOOD, GOOD, GOOD, GOOD, GOOD, 3, 3, 0)
-    rope = c.RopeDesc(GOOD, GOOD, 8, 1, 0, 1)
+    cache = CacheDesc(4, 2, 16, 64, GOOD, GOOD, GOOD, GOOD, GOOD, 3, 3, 0)
+    rope = RopeDesc(GOOD, GOOD, 8, 1, 0, 1)
     rope.axis_pairs[0] = 16
     rope.scale = 1.0
     return rows, cache, rope
@@ -178,8 +211,7 @@ def test_binding_refuses_wrong_tensors(sfa):
 
 
 def _attn(sfa):
-    from frame_sparse_attention_b200 import _cache as c
-    d = c.CacheAttnDesc(2, 4, 2, 8, 64, 0.125, 0, 0)
+    d = CacheAttnDesc(2, 4, 2, 8, 64, 0.125, 0, 0)
     for t in ("q", "o"):
         for i, s in enumerate((4 * 8 * 64, 8 * 64, 64)):
             setattr(d, f"{t}_stride{i}", s)
