@@ -28,6 +28,8 @@ namespace sfa {
 namespace {
 
 constexpr int ROW_WARPS = 8;  // warps per CTA
+constexpr int ROW_CTAS = 4;   // CTAs per SM: 64 registers a thread, 32 warps (24 warps with 80: 154 against 143 us
+                              // on 63960 tokens of 12 + 12 heads, and 33 against 29 on the append of 4680)
 
 struct RowsArgs {
     int32_t B, H, Hk, L;
@@ -50,7 +52,7 @@ struct RowsArgs {
     const int32_t *lens;
     int32_t *status;
     int32_t n_parts;   // warps per token
-    int64_t n_warps;   // B * L * n_parts
+    uint32_t n_warps;  // B * L * n_parts
 };
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -70,28 +72,90 @@ __device__ __forceinline__ float2 rotation(const RowsArgs &a, const int32_t *pos
     return make_float2(c * a.rope_scale, s * a.rope_scale);
 }
 
-// y = rs * (x * A + x_partner * B) for this lane's eight elements
+// Two fp32 numbers that one instruction works on (each rounds like a scalar).
+__device__ __forceinline__ uint64_t f2(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi2(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// A lane's eight elements as pairs of even ones, (0, 2) and (4, 6), and of odd ones, (1, 3) and
+// (5, 7): the two elements of an interleaved rotation pair lie in the same place of e and o.
+struct Eight {
+    uint64_t e[2], o[2];
+};
+__device__ __forceinline__ Eight unpack8(const uint32_t (&w)[4])
+{
+    Eight x;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        x.e[i] = f2(bf_lo(w[2 * i]), bf_lo(w[2 * i + 1]));
+        x.o[i] = f2(bf_hi(w[2 * i]), bf_hi(w[2 * i + 1]));
+    }
+    return x;
+}
+
+// y = rs * (x * A + mate * B) for this lane's elements
 struct Coef {
-    float A[8], B[8];
+    Eight A, B;
 };
 
 template <int D, bool HALF>
-__device__ __forceinline__ void coefficients(Coef &f, const float2 *cs, const float *w, int e0, int R)
+__device__ __forceinline__ void coefficients(Coef &f, const float *cosp, const float *sinp, const float *w, int e0, int R)
 {
+    float A[8], B[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int e = e0 + j;
-        const float we = w ? __ldg(w + e) : 1.f;
-        f.A[j] = we;
-        f.B[j] = 0.f;
-        if (e < R) {
-            const bool first = HALF ? e < R / 2 : (j & 1) == 0;
-            const int mate = HALF ? (first ? e + R / 2 : e - R / 2) : (e ^ 1);
-            const float2 r = cs[HALF ? (first ? e : mate) : e >> 1];
-            const float wm = w ? __ldg(w + mate) : 1.f;
-            f.A[j] = we * r.x;
-            f.B[j] = first ? -wm * r.y : wm * r.y;
+        A[j] = 1.f;
+        B[j] = 0.f;
+    }
+    const bool first = HALF && e0 < R / 2;
+    const int mate0 = !HALF ? e0 : first ? e0 + R / 2 : e0 < R ? e0 - R / 2 : e0;  // where the mates' weights lie
+    float wo[8], wm[8];
+    if (w) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+            const float4 x = __ldg(reinterpret_cast<const float4 *>(w + e0 + j));
+            const float4 y = HALF ? __ldg(reinterpret_cast<const float4 *>(w + mate0 + j)) : x;
+            wo[j] = x.x, wo[j + 1] = x.y, wo[j + 2] = x.z, wo[j + 3] = x.w;
+            wm[j] = y.x, wm[j + 1] = y.y, wm[j + 2] = y.z, wm[j + 3] = y.w;
         }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) wo[j] = wm[j] = 1.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        A[j] = wo[j];
+        if (e0 + j < R) {
+            const int p = HALF ? (first ? e0 : mate0) + j : (e0 + j) >> 1;
+            const float c = cosp[p], s = sinp[p];
+            A[j] = wo[j] * c;
+            const bool minus = HALF ? first : (j & 1) == 0;
+            B[j] = (HALF ? wm[j] : wo[j ^ 1]) * (minus ? -s : s);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        f.A.e[i] = f2(A[4 * i], A[4 * i + 2]);
+        f.A.o[i] = f2(A[4 * i + 1], A[4 * i + 3]);
+        f.B.e[i] = f2(B[4 * i], B[4 * i + 2]);
+        f.B.o[i] = f2(B[4 * i + 1], B[4 * i + 3]);
     }
 }
 
@@ -101,40 +165,56 @@ __device__ __forceinline__ uint4 norm_rotate(const uint4 raw, const Coef &f, flo
 {
     constexpr int G = D / 8;
     const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        x[2 * j] = bf_lo(in[j]);
-        x[2 * j + 1] = bf_hi(in[j]);
-    }
+    const Eight x = unpack8(in);
     float rs = 1.f;
     if (eps >= 0.f) {
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+        const uint64_t s = fma2(x.o[1], x.o[1], fma2(x.e[1], x.e[1], fma2(x.o[0], x.o[0], mul2(x.e[0], x.e[0]))));
+        float ss = lo2(s) + hi2(s);
 #pragma unroll
         for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         rs = rsqrtf(ss * (1.f / D) + eps);
     }
-    float y[8];
+    // an interleaved mate is the other element of the pair; the mates of half a row are the
+    // eight elements of the lane R/16 further on or back
+    Eight m;
     if (HALF) {
-        // the partners are the eight elements of the lane R/16 further on or back
         const int lane = threadIdx.x & 31;
         const int src = e0 < R / 2 ? lane + R / 16 : (e0 < R ? lane - R / 16 : lane);
-        uint32_t m[4];
+        uint32_t mw[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) m[j] = __shfl_sync(0xffffffffu, in[j], src);
+        for (int j = 0; j < 4; ++j) mw[j] = __shfl_sync(0xffffffffu, in[j], src);
+        if (R < D) {  // elements that do not turn have no mate, whatever the numbers there
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float mate = (j & 1) ? bf_hi(m[j >> 1]) : bf_lo(m[j >> 1]);
-            y[j] = rs * (x[j] * f.A[j] + (e0 < R ? mate * f.B[j] : 0.f));
+            for (int j = 0; j < 4; ++j) mw[j] = e0 < R ? mw[j] : 0u;
+        }
+        m = unpack8(mw);
+    } else if (R < D) {
+        uint32_t mw[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mw[j] = e0 + 2 * j < R ? in[j] : 0u;
+        const Eight z = unpack8(mw);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            m.e[i] = z.o[i];
+            m.o[i] = z.e[i];
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = rs * (x[j] * f.A[j] + (e0 + j < R ? x[j ^ 1] * f.B[j] : 0.f));
+        for (int i = 0; i < 2; ++i) {
+            m.e[i] = x.o[i];
+            m.o[i] = x.e[i];
+        }
     }
-    return make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                      pack_bf16x2(y[6], y[7]));
+    const uint64_t r2 = f2(rs, rs);
+    uint32_t out[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint64_t ye = mul2(r2, fma2(m.e[i], f.B.e[i], mul2(x.e[i], f.A.e[i])));
+        const uint64_t yo = mul2(r2, fma2(m.o[i], f.B.o[i], mul2(x.o[i], f.A.o[i])));
+        out[2 * i] = pack_bf16x2(lo2(ye), lo2(yo));
+        out[2 * i + 1] = pack_bf16x2(hi2(ye), hi2(yo));
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 // Largest magnitude (bf16 bits) of the block of 32 elements that this lane and its three
@@ -178,9 +258,16 @@ __device__ __forceinline__ void store_row(uint8_t *codes, uint8_t *scales, int64
     }
     const int e = block_exponent(top);
     const float inv = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e; the products are exact
-    uint2 c;
-    c.x = to_e4m3x2(bf_lo(w[0]) * inv, bf_hi(w[0]) * inv) | (to_e4m3x2(bf_lo(w[1]) * inv, bf_hi(w[1]) * inv) << 16);
-    c.y = to_e4m3x2(bf_lo(w[2]) * inv, bf_hi(w[2]) * inv) | (to_e4m3x2(bf_lo(w[3]) * inv, bf_hi(w[3]) * inv) << 16);
+    const uint64_t inv2 = f2(inv, inv);
+    const Eight x = unpack8(w);
+    uint32_t c4[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint64_t ye = mul2(x.e[i], inv2), yo = mul2(x.o[i], inv2);
+        c4[2 * i] = to_e4m3x2(lo2(ye), lo2(yo));
+        c4[2 * i + 1] = to_e4m3x2(hi2(ye), hi2(yo));
+    }
+    const uint2 c = make_uint2(c4[0] | (c4[1] << 16), c4[2] | (c4[3] << 16));
     if (row >= 0) {
         *reinterpret_cast<uint2 *>(codes + row * D + e0) = c;
         if ((e0 & (CACHE_BLOCK - 1)) == 0) scales[row * (D / CACHE_BLOCK) + e0 / CACHE_BLOCK] = (uint8_t)(e + 127);
@@ -189,95 +276,121 @@ __device__ __forceinline__ void store_row(uint8_t *codes, uint8_t *scales, int64
 
 // One warp per token, or one of n_parts warps that share a token's row groups: groups
 // [0, Gq) are the query heads, [Gq, Gq + Gk) the key (and value) heads, RW heads a group,
-// and part p takes the groups g = p mod n_parts.
+// and part p takes the groups g = p mod n_parts.  The loads of the first U groups go out
+// before the angles are formed, and a group's registers are loaded again as soon as it is
+// done, so a warp has U (CACHE: a pair of) rows under way throughout.
 template <int D, bool HALF, bool CACHE>
-__global__ void __launch_bounds__(ROW_WARPS * 32) rows_kernel(const __grid_constant__ RowsArgs a)
+__global__ void __launch_bounds__(ROW_WARPS * 32, ROW_CTAS) rows_kernel(const __grid_constant__ RowsArgs a)
 {
     constexpr int G = D / 8;     // lanes per row
     constexpr int RW = 32 / G;   // rows of a group
-    constexpr int UQ = 4;        // groups loaded before any arithmetic
-    constexpr int UK = CACHE ? 2 : 4;
-    __shared__ float2 cs_all[ROW_WARPS][D / 2];
+    constexpr int U = CACHE ? 2 : 4;  // groups under way (append, U = 4: 31 against 29 us)
+    __shared__ float cos_all[ROW_WARPS][D / 2], sin_all[ROW_WARPS][D / 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t w = (int64_t)blockIdx.x * ROW_WARPS + warp;
+    const uint32_t w = blockIdx.x * (uint32_t)ROW_WARPS + warp;
     if (w >= a.n_warps) return;
-    const int64_t token = w / a.n_parts;
+    const uint32_t token = a.n_parts == 1 ? w : w / (uint32_t)a.n_parts;
     const int part = (int)(w - token * a.n_parts);
-    const int b = (int)(token / a.L), i = (int)(token - (int64_t)b * a.L);
+    const int b = (int)(token / (uint32_t)a.L), i = (int)(token - b * (uint32_t)a.L);
     if (a.lens && i >= __ldg(a.lens + b)) return;  // a padded row (the whole warp)
-    float2 *cs = cs_all[warp];
-    const int32_t *pos = a.R ? a.pos + b * a.ps0 + i * a.ps1 : nullptr;
-    for (int p = lane; p < a.R / 2; p += 32) cs[p] = rotation(a, pos, p);
-    __syncwarp();
     const int sub = lane / G, e0 = (lane % G) * 8;
     const int Gq = a.q ? (a.H + RW - 1) / RW : 0;
     const int Gk = (a.k || a.v) ? (a.Hk + RW - 1) / RW : 0;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const int step = a.n_parts;
+
+    const uint16_t *q_src = a.q + b * a.qs[0] + i * a.qs[2] + e0;
+    auto load_q = [&](int g) {
+        const int h = g * RW + sub;
+        return g < Gq && h < a.H ? *reinterpret_cast<const uint4 *>(q_src + h * a.qs[1]) : zero;
+    };
+    const uint16_t *k_src = a.k + b * a.ks[0] + i * a.ks[2] + e0, *v_src = a.v + b * a.vs[0] + i * a.vs[2] + e0;
+    auto load_k = [&](int g) {
+        const int h = g * RW + sub;
+        return g < Gk && h < a.Hk ? *reinterpret_cast<const uint4 *>(k_src + h * a.ks[1]) : zero;
+    };
+    auto load_v = [&](int g) {
+        const int h = g * RW + sub;
+        return g < Gk && h < a.Hk ? *reinterpret_cast<const uint4 *>(v_src + h * a.vs[1]) : zero;
+    };
+    uint4 x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = load_q(part + u * step);
+
+    float *cosp = cos_all[warp], *sinp = sin_all[warp];
+    const int32_t *pos = a.R ? a.pos + b * a.ps0 + i * a.ps1 : nullptr;
+    for (int p = lane; p < a.R / 2; p += 32) {
+        const float2 r = rotation(a, pos, p);
+        cosp[p] = r.x;
+        sinp[p] = r.y;
+    }
+    __syncwarp();
 
     Coef f;
     if (part < Gq) {
-        coefficients<D, HALF>(f, cs, a.q_weight, e0, a.R);
-        const uint16_t *src = a.q + b * a.qs[0] + i * a.qs[2] + e0;
+        coefficients<D, HALF>(f, cosp, sinp, a.q_weight, e0, a.R);
         uint16_t *dst = a.q_out + b * a.qo[0] + i * a.qo[2] + e0;
-        for (int g0 = part; g0 < Gq; g0 += UQ * a.n_parts) {
-            uint4 x[UQ];
+        for (int g0 = part; g0 < Gq; g0 += U * step) {
 #pragma unroll
-            for (int u = 0; u < UQ; ++u) {
-                const int h = (g0 + u * a.n_parts) * RW + sub;
-                x[u] = h < a.H ? *reinterpret_cast<const uint4 *>(src + h * a.qs[1]) : zero;
-            }
-#pragma unroll
-            for (int u = 0; u < UQ; ++u) {
-                const int h = (g0 + u * a.n_parts) * RW + sub;
+            for (int u = 0; u < U; ++u) {
+                const int g = g0 + u * step, h = g * RW + sub;
+                if (g >= Gq) break;
                 const uint4 y = norm_rotate<D, HALF>(x[u], f, a.eps, e0, a.R);
+                x[u] = load_q(g + U * step);
                 if (h < a.H) *reinterpret_cast<uint4 *>(dst + h * a.qo[1]) = y;
             }
         }
     }
     // this part's first key group: g + Gq = part mod n_parts
-    const int first = (part + a.n_parts - Gq % a.n_parts) % a.n_parts;
+    const int first = (part + step - Gq % step) % step;
     if (first >= Gk) return;
     const bool plain = a.eps < 0.f && a.R == 0 && !a.k_weight;  // keys stored as they are
-    if (!plain) coefficients<D, HALF>(f, cs, a.k_weight, e0, a.R);
-    const uint16_t *k_src = a.k + b * a.ks[0] + i * a.ks[2] + e0;
     if (!CACHE) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] = load_k(first + u * step);
+        coefficients<D, HALF>(f, cosp, sinp, a.k_weight, e0, a.R);
         uint16_t *dst = a.k_out + b * a.ko[0] + i * a.ko[2] + e0;
-        for (int g0 = first; g0 < Gk; g0 += UK * a.n_parts) {
-            uint4 x[UK];
+        for (int g0 = first; g0 < Gk; g0 += U * step) {
 #pragma unroll
-            for (int u = 0; u < UK; ++u) {
-                const int h = (g0 + u * a.n_parts) * RW + sub;
-                x[u] = h < a.Hk ? *reinterpret_cast<const uint4 *>(k_src + h * a.ks[1]) : zero;
-            }
-#pragma unroll
-            for (int u = 0; u < UK; ++u) {
-                const int h = (g0 + u * a.n_parts) * RW + sub;
+            for (int u = 0; u < U; ++u) {
+                const int g = g0 + u * step, h = g * RW + sub;
+                if (g >= Gk) break;
                 const uint4 y = norm_rotate<D, HALF>(x[u], f, a.eps, e0, a.R);
+                x[u] = load_k(g + U * step);
                 if (h < a.Hk) *reinterpret_cast<uint4 *>(dst + h * a.ko[1]) = y;
             }
         }
     } else {
-        const uint16_t *v_src = a.v + b * a.vs[0] + i * a.vs[2] + e0;
-        for (int g0 = first; g0 < Gk; g0 += UK * a.n_parts) {
-            uint4 x[UK], y[UK];
-            int64_t row[UK];
+        constexpr int UK = U / 2;
+        uint4 y[UK];
+        int start[UK];  // of the group's heads
+        auto load_start = [&](int g) {
+            const int h = min(g * RW + sub, a.Hk - 1);
+            return __ldg(a.start + b * a.ss0 + h * a.ss1);
+        };
+#pragma unroll
+        for (int u = 0; u < UK; ++u) {
+            x[u] = load_k(first + u * step);
+            y[u] = load_v(first + u * step);
+            start[u] = load_start(first + u * step);
+        }
+        if (!plain) coefficients<D, HALF>(f, cosp, sinp, a.k_weight, e0, a.R);
+        for (int g0 = first; g0 < Gk; g0 += UK * step) {
 #pragma unroll
             for (int u = 0; u < UK; ++u) {
-                const int h = (g0 + u * a.n_parts) * RW + sub;
-                const bool on = h < a.Hk;
-                x[u] = on ? *reinterpret_cast<const uint4 *>(k_src + h * a.ks[1]) : zero;
-                y[u] = on ? *reinterpret_cast<const uint4 *>(v_src + h * a.vs[1]) : zero;
-                row[u] = -1;
-                if (on) {
-                    row[u] = cache_row(a.cache, b, h, (int64_t)__ldg(a.start + b * a.ss0 + h * a.ss1) + i);
-                    if (row[u] < 0) report_status(a.status, SFA_ERR_BAD_SET);
+                const int g = g0 + u * step, h = g * RW + sub;
+                if (g >= Gk) break;
+                int64_t row = -1;
+                if (h < a.Hk) {
+                    row = cache_row(a.cache, b, h, (int64_t)start[u] + i);
+                    if (row < 0) report_status(a.status, SFA_ERR_BAD_SET);
                 }
-            }
-#pragma unroll
-            for (int u = 0; u < UK; ++u) {
-                if (!plain) x[u] = norm_rotate<D, HALF>(x[u], f, a.eps, e0, a.R);
-                store_row<D>(a.cache.k, a.cache.k_scale, row[u], x[u], e0, a.status);
-                store_row<D>(a.cache.v, a.cache.v_scale, row[u], y[u], e0, a.status);
+                const uint4 kk = plain ? x[u] : norm_rotate<D, HALF>(x[u], f, a.eps, e0, a.R), vv = y[u];
+                x[u] = load_k(g + UK * step);
+                y[u] = load_v(g + UK * step);
+                start[u] = load_start(g + UK * step);
+                store_row<D>(a.cache.k, a.cache.k_scale, row, kk, e0, a.status);
+                store_row<D>(a.cache.v, a.cache.v_scale, row, vv, e0, a.status);
             }
         }
     }
@@ -292,7 +405,7 @@ struct ReadArgs {
     uint16_t *k_out, *v_out;
     int64_t ko[3], vo[3];
     int32_t *status;
-    int64_t rows;  // B * Hk * L
+    uint32_t rows;  // B * Hk * L
 };
 
 // Eight codes and their block's scale -> eight bf16 numbers.
@@ -312,40 +425,39 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__
 {
     constexpr int G = D / 8;  // lanes per row
     constexpr int U = 4;      // rows per lane group, all their loads issued first
-    const int64_t group = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / G;
-    const int64_t n_groups = (int64_t)gridDim.x * blockDim.x / G;
+    const uint32_t group = (blockIdx.x * blockDim.x + threadIdx.x) / G;
+    const uint32_t n_groups = gridDim.x * blockDim.x / G;
     const int e0 = (threadIdx.x % G) * 8;
-    for (int64_t r0 = group; r0 < a.rows; r0 += n_groups * U) {
-        uint2 kc[U], vc[U];
-        uint32_t ks[U], vs[U];
-        int64_t row[U];
+    uint2 kc[U], vc[U];
+    uint32_t ks[U], vs[U];
+    int64_t row[U];
+    int b[U], h[U], i[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t r = r0 + u * n_groups;
-            row[u] = -1;
-            if (r >= a.rows) continue;
-            const int64_t bh = r / a.L;
-            const int i = (int)(r - bh * a.L), b = (int)(bh / a.Hk), h = (int)(bh - (int64_t)b * a.Hk);
-            if (a.lens && i >= __ldg(a.lens + b)) continue;
-            row[u] = cache_row(a.cache, b, h, (int64_t)__ldg(a.start + b * a.ss0 + h * a.ss1) + i);
-            if (row[u] < 0) {
-                report_status(a.status, SFA_ERR_BAD_SET);
-                continue;
-            }
-            kc[u] = *reinterpret_cast<const uint2 *>(a.cache.k + row[u] * D + e0);
-            vc[u] = *reinterpret_cast<const uint2 *>(a.cache.v + row[u] * D + e0);
-            ks[u] = a.cache.k_scale[row[u] * (D / CACHE_BLOCK) + e0 / CACHE_BLOCK];
-            vs[u] = a.cache.v_scale[row[u] * (D / CACHE_BLOCK) + e0 / CACHE_BLOCK];
-        }
+    for (int u = 0; u < U; ++u) {
+        const uint32_t r = group + u * n_groups;
+        row[u] = -1;
+        if (r >= a.rows) continue;
+        const uint32_t bh = r / (uint32_t)a.L;
+        i[u] = (int)(r - bh * (uint32_t)a.L);
+        b[u] = (int)(bh / (uint32_t)a.Hk);
+        h[u] = (int)(bh - b[u] * (uint32_t)a.Hk);
+        if (a.lens && i[u] >= __ldg(a.lens + b[u])) continue;
+        row[u] = cache_row(a.cache, b[u], h[u], (int64_t)__ldg(a.start + b[u] * a.ss0 + h[u] * a.ss1) + i[u]);
+        if (row[u] < 0) report_status(a.status, SFA_ERR_BAD_SET);
+    }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (row[u] < 0) continue;
-            const int64_t r = r0 + u * n_groups;
-            const int64_t bh = r / a.L;
-            const int64_t i = r - bh * a.L, b = bh / a.Hk, h = bh - b * a.Hk;
-            *reinterpret_cast<uint4 *>(a.k_out + b * a.ko[0] + h * a.ko[1] + i * a.ko[2] + e0) = from_codes(kc[u], ks[u]);
-            *reinterpret_cast<uint4 *>(a.v_out + b * a.vo[0] + h * a.vo[1] + i * a.vo[2] + e0) = from_codes(vc[u], vs[u]);
-        }
+    for (int u = 0; u < U; ++u) {
+        const int64_t r = row[u] < 0 ? 0 : row[u];  // (row 0 is always there: no branch parts the loads)
+        kc[u] = load_codes8(a.cache.k + r * D + e0);
+        vc[u] = load_codes8(a.cache.v + r * D + e0);
+        ks[u] = __ldg(a.cache.k_scale + r * (D / CACHE_BLOCK) + e0 / CACHE_BLOCK);
+        vs[u] = __ldg(a.cache.v_scale + r * (D / CACHE_BLOCK) + e0 / CACHE_BLOCK);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (row[u] < 0) continue;
+        *reinterpret_cast<uint4 *>(a.k_out + b[u] * a.ko[0] + h[u] * a.ko[1] + i[u] * a.ko[2] + e0) = from_codes(kc[u], ks[u]);
+        *reinterpret_cast<uint4 *>(a.v_out + b[u] * a.vo[0] + h[u] * a.vo[1] + i[u] * a.vo[2] + e0) = from_codes(vc[u], vs[u]);
     }
 }
 
@@ -355,6 +467,12 @@ int device_sms()
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     return sms > 0 ? sms : 148;
+}
+
+// norm weights are read 16 bytes at a time
+bool weights_ok(const float *q, const float *k)
+{
+    return reinterpret_cast<uintptr_t>(q) % 16 == 0 && reinterpret_cast<uintptr_t>(k) % 16 == 0;
 }
 
 bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -419,9 +537,9 @@ sfa_status launch_rows(RowsArgs &a, int d, bool half, cudaStream_t s)
     // with 32 warps each, else as many as fill them, at most one per row group.
     const int64_t want = ((int64_t)device_sms() * 32 + tokens - 1) / tokens;
     a.n_parts = (int32_t)(want < 1 ? 1 : (want > groups ? groups : want));
-    a.n_warps = tokens * a.n_parts;
-    const int64_t grid = (a.n_warps + ROW_WARPS - 1) / ROW_WARPS;
-    if (tokens >= ((int64_t)1 << 31) || grid >= ((int64_t)1 << 31)) return SFA_ERR_INVALID_ARG;
+    if (tokens >= ((int64_t)1 << 31)) return SFA_ERR_INVALID_ARG;  // (parts: only where tokens are few)
+    a.n_warps = (uint32_t)tokens * (uint32_t)a.n_parts;
+    const int64_t grid = ((int64_t)a.n_warps + ROW_WARPS - 1) / ROW_WARPS;
     const dim3 g((unsigned)grid), t(ROW_WARPS * 32);
     if (d == 128 && half) rows_kernel<128, true, CACHE><<<g, t, 0, s>>>(a);
     else if (d == 128) rows_kernel<128, false, CACHE><<<g, t, 0, s>>>(a);
@@ -469,7 +587,8 @@ extern "C" sfa_status sfa_qk_norm_rope(const sfa_rows_desc *d, const sfa_rope *r
     if (d->B == 0 || d->L == 0) return SFA_OK;
     if ((!q && !k) || !q != !q_out || !k != !k_out) return SFA_ERR_INVALID_ARG;
     if ((q && !heads_ok(d->H)) || (k && !heads_ok(d->H_kv))) return SFA_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out)) return SFA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out) || !weights_ok(q_weight, k_weight))
+        return SFA_ERR_INVALID_ARG;
     if (q && (!rows_stride_ok(d->q_stride, d->B, d->H, d->L) || !rows_stride_ok(d->q_out_stride, d->B, d->H, d->L)))
         return SFA_ERR_INVALID_ARG;
     if (k && (!rows_stride_ok(d->k_stride, d->B, d->H_kv, d->L) || !rows_stride_ok(d->k_out_stride, d->B, d->H_kv, d->L)))
@@ -527,7 +646,8 @@ extern "C" sfa_status sfa_cache_append(const sfa_rows_desc *d, const sfa_rope *r
     st = check_cache_rows(d, cache, start);
     if (st != SFA_OK) return st;
     if (!q || !k || !v || !q_out || !heads_ok(d->H)) return SFA_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out)) return SFA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !weights_ok(q_weight, k_weight))
+        return SFA_ERR_INVALID_ARG;
     if (!rows_stride_ok(d->q_stride, d->B, d->H, d->L) || !rows_stride_ok(d->q_out_stride, d->B, d->H, d->L) ||
         !rows_stride_ok(d->k_stride, d->B, d->H_kv, d->L) || !rows_stride_ok(d->v_stride, d->B, d->H_kv, d->L))
         return SFA_ERR_INVALID_ARG;
@@ -574,11 +694,11 @@ extern "C" sfa_status sfa_cache_read(const sfa_rows_desc *d, const sfa_cache *ca
     copy3(a.ko, d->k_out_stride);
     copy3(a.vo, d->v_out_stride);
     a.status = dev_status;
-    a.rows = (int64_t)d->B * d->H_kv * d->L;
-    if ((int64_t)d->B * d->L >= ((int64_t)1 << 31)) return SFA_ERR_INVALID_ARG;
+    const int64_t rows = (int64_t)d->B * d->H_kv * d->L;
+    if ((int64_t)d->B * d->L >= ((int64_t)1 << 31) || rows >= ((int64_t)1 << 31)) return SFA_ERR_INVALID_ARG;
+    a.rows = (uint32_t)rows;
     const int per_cta = 256 / (d->d / 8) * 4;
-    const int64_t need = (a.rows + per_cta - 1) / per_cta;
-    const int64_t grid = need < (int64_t)1 << 30 ? need : (int64_t)1 << 30;
+    const int64_t grid = (rows + per_cta - 1) / per_cta;
     if (d->d == 128) cache_read_kernel<128><<<(unsigned)grid, 256, 0, as_cuda(stream)>>>(a);
     else cache_read_kernel<64><<<(unsigned)grid, 256, 0, as_cuda(stream)>>>(a);
     return launch_status();

@@ -542,8 +542,8 @@ typedef struct {
 
 /*
  * Norm and rotation of queries and keys in one pass:
- *   y = x / sqrt(mean(x^2) + eps) * weight  (per head row; weight fp32 [d] or NULL = ones;
- *   no norm with eps < 0), then the rotation (rope NULL: none), in fp32, rounded to bf16 once.
+ *   y = x / sqrt(mean(x^2) + eps) * weight  (per head row; weight fp32 [d], 16-byte aligned,
+ *   or NULL = ones; no norm with eps < 0), then the rotation (rope NULL: none), in fp32, rounded to bf16 once.
  * q or k may be NULL (with its output).  q_out / k_out may be q / k themselves (same strides).
  */
 sfa_status sfa_qk_norm_rope(const sfa_rows_desc *desc, const sfa_rope *rope, const void *q, const void *k,

@@ -169,6 +169,14 @@ def test_norm_rope_needs_an_input_and_its_output(sfa):
     assert lib.sfa_qk_norm_rope(r, None, GOOD, None, None, None, GOOD, GOOD, None) == 1
 
 
+def test_weights_are_aligned(sfa):
+    lib, r = sfa.load(), ctypes.byref
+    rows, cache, rope = _structs()
+    for w in ((GOOD + 4, None), (None, GOOD + 8)):
+        assert lib.sfa_qk_norm_rope(r(rows), r(rope), GOOD, GOOD, *w, GOOD, GOOD, None) == 1
+        assert lib.sfa_cache_append(r(rows), r(rope), r(cache), GOOD, GOOD, GOOD, *w, GOOD, GOOD, None, None, None) == 1
+
+
 def test_binding_refuses_wrong_tensors(sfa):
     q = torch.zeros(2, 4, 8, 64, dtype=torch.bfloat16)
     k = torch.zeros(2, 2, 8, 64, dtype=torch.bfloat16)
