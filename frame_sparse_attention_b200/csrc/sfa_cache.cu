@@ -533,9 +533,11 @@ sfa_status launch_rows(RowsArgs &a, int d, bool half, cudaStream_t s)
     const int rw = 32 / (d / 8);
     const int groups = (a.q ? (a.H + rw - 1) / rw : 0) + ((a.k || a.v) ? (a.Hk + rw - 1) / rw : 0);
     const int64_t tokens = (int64_t)a.B * a.L;
-    // Warps per token: one (the angles are formed once) while the tokens alone fill the SMs
-    // with 32 warps each, else as many as fill them, at most one per row group.
-    const int64_t want = ((int64_t)device_sms() * 32 + tokens - 1) / tokens;
+    // Warps per token: one (the angles are formed once) while the tokens alone give every SM
+    // 16 warps, else as many as do, at most one per row group.  (Norm and rotation of 12 + 12
+    // heads with 8, 16, 32 and 64 warps an SM: 200 tokens of 8 sequences 8.2, 7.4, 9.4 and
+    // 12.3 us; 1560 tokens 7.6, 6.8, 9.3 and 12.5; 4680 tokens 13.6, 13.7, 16.9 and 20.3.)
+    const int64_t want = ((int64_t)device_sms() * 16 + tokens - 1) / tokens;
     a.n_parts = (int32_t)(want < 1 ? 1 : (want > groups ? groups : want));
     if (tokens >= ((int64_t)1 << 31)) return SFA_ERR_INVALID_ARG;  // (parts: only where tokens are few)
     a.n_warps = (uint32_t)tokens * (uint32_t)a.n_parts;
