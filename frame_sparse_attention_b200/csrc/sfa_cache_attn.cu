@@ -95,7 +95,8 @@ __device__ __forceinline__ int n_ranges(const ChunkArgs &a, int steps)
 // Row `id` of the outputs: (b * H + h) * Lq + i for row r of a unit.
 __device__ __forceinline__ int64_t row_id(const ChunkArgs &a, const Unit &u, int r)
 {
-    return ((int64_t)u.b * a.H + u.hk * a.G + r % a.G) * a.Lq + r / a.G;
+    const int tok = a.G == 1 ? r : r / a.G;
+    return ((int64_t)u.b * a.H + u.hk * a.G + (r - tok * a.G)) * a.Lq + tok;
 }
 
 // A CTA without a range of its own leaves "nothing seen" for its rows.
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(FR_WARPS * 32, 4) rows_attn_kernel(const __gri
 // (with P in shared memory, as in the frame-list kernel, a key tile took 5600 cycles, 2200 of
 // them in the issue of 11 loads behind blocked stores).  So P stays in tensor memory, in the
 // columns of the S that it comes from, as the first operand of P V.
-constexpr int CT_SOFTMAX_WARPS = 8;       // warps 0-3: query tile A, 4-7: B
+// warps 0-3: softmax of query tile A, 4-7: of B
 constexpr int CT_K_WARP = 8;              // 8-11: codes of K to bf16
 constexpr int CT_V_WARP = 12;             // 12-14: of V
 constexpr int CT_MMA_WARP = 15;
@@ -484,11 +485,10 @@ struct CBars {
     __device__ uint32_t v_free(int s) const { return base + 8 * (2 * NSK + NSV + s); }
     __device__ uint32_t s_full(int x) const { return base + 8 * (2 * NSK + 2 * NSV + x); }      // S of tile x
     __device__ uint32_t p_full(int x) const { return base + 8 * (2 * NSK + 2 * NSV + 2 + x); }  // P of tile x
-    __device__ uint32_t q_full() const { return base + 8 * (2 * NSK + 2 * NSV + 4); }
-    __device__ uint32_t o_final() const { return base + 8 * (2 * NSK + 2 * NSV + 5); }  // after the last P V
-    __device__ uint32_t pv_done() const { return base + 8 * (2 * NSK + 2 * NSV + 6); }  // one-tile units: a P V
-    __device__ uint32_t drain() const { return base + 8 * (2 * NSK + 2 * NSV + 7); }
-    static constexpr int COUNT = 2 * NSK + 2 * NSV + 8;
+    __device__ uint32_t o_final() const { return base + 8 * (2 * NSK + 2 * NSV + 4); }  // after the last P V
+    __device__ uint32_t pv_done() const { return base + 8 * (2 * NSK + 2 * NSV + 5); }  // one-tile units: a P V
+    __device__ uint32_t drain() const { return base + 8 * (2 * NSK + 2 * NSV + 6); }
+    static constexpr int COUNT = 2 * NSK + 2 * NSV + 7;
     static_assert(8 * COUNT <= 160, "mbarriers end before the flags at +160");
 };
 
@@ -499,13 +499,22 @@ __device__ __forceinline__ uint32_t swz(int r, int ch)
     return (uint32_t)((ch >> 3) * Cfg<D>::BOX_BYTES + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
 }
 
+// The barriers and tensor memory are there from here on.  Every warp passes it once, from its
+// role's code: what it can load before, it has under way by then.
+__device__ __forceinline__ void block_meets()
+{
+    tc_fence_before();
+    named_bar_sync(0, CT_THREADS);
+    tc_fence_after();
+}
+
 // The K (IS_K) or V tiles of the unit, codes to bf16.  D/16 lanes share a row, 16 codes each,
 // and the tile's rows go round the warps, RPI at a time.  A lane looks up one row's place (two
 // where a warp has more than 32 rows).  The next tile's codes are on their way while the warp
 // waits for its slot.
 template <int D, bool IS_K>
 __device__ void convert_role(const ChunkArgs &a, const Unit &u, uint32_t sbase, int key0, int key_end, int n_tiles,
-                             const Ctl &ctl)
+                             const volatile int32_t *skip, const Ctl &ctl)
 {
     using C = CCfg<D>;
     constexpr int NS = IS_K ? C::NSK : C::NSV;
@@ -600,6 +609,8 @@ __device__ void convert_role(const ChunkArgs &a, const Unit &u, uint32_t sbase, 
     look_up(0);
     load();
     look_up(1);
+    block_meets();
+    if (*skip) return;
     for (int j = 0; j < n_tiles; ++j) {
         bool two = false;
 #pragma unroll
@@ -643,7 +654,6 @@ __device__ void chunk_mma(uint32_t sbase, uint32_t tmem, int n_tiles, const Ctl 
         if (last_reader) commit_one(bar.k_free(sk));
         issued = true;
     };
-    if (!__all_sync(0xffffffffu, wait_bar(bar.q_full(), 0, ctl))) goto done;
     for (int x = 0; x < 2; ++x) {
         const int j = PAIR ? 0 : x;
         if (j >= n_tiles) break;
@@ -753,8 +763,9 @@ __device__ __forceinline__ bool chunk_softmax_tile(uint32_t t_s, uint32_t t_o, i
 
 // Queries, softmax and epilogue of query tile x, one thread per row.
 template <int D>
-__device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *smem, uint32_t sbase, uint32_t tmem, int x,
-                                   int key0, int n_tiles, bool one_tile, const Ctl &ctl)
+__device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *smem, uint32_t sbase,
+                                   const volatile uint32_t *tmem_slot, const volatile int32_t *skip, int x, int key0,
+                                   int n_tiles, bool one_tile, const Ctl &ctl)
 {
     using C = CCfg<D>;
     constexpr int LR = D / 8;     // lanes per 16-byte-pieced row
@@ -764,21 +775,32 @@ __device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *s
     const int row = threadIdx.x & 127, lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
     const int tile_row0 = u.row0 + x * BM;
     const uint32_t s_tile = sbase + C::SMEM_Q + x * C::TILE_BYTES;
-    // this warp's 32 query rows, whole rows at a time
-#pragma unroll 8
-    for (int i = 0; i < 32; i += RPI) {
-        const int rr = warp * 32 + i + lane / LR, ch = lane % LR, r = tile_row0 + rr;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (r < u.n_rows)
-            v = *reinterpret_cast<const uint4 *>(a.q + u.b * a.qs[0] + (u.hk * a.G + r % a.G) * a.qs[1] +
-                                                 (r / a.G) * a.qs[2] + ch * 8);
-        const uint32_t y[4] = {v.x, v.y, v.z, v.w};
-        st_shared_v4(s_tile + swz<D>(rr, ch), y);
+    // fp32 rows of a partial result: twice a tile's bytes, in the query tiles' and K slots' place,
+    // which nothing reads any more after the last product
+    const uint32_t s_part = sbase + C::SMEM_Q + x * 2 * C::TILE_BYTES;
+    static_assert(C::SMEM_V >= 4 * C::TILE_BYTES, "two tiles of fp32 rows end before the V slots");
+    // this warp's 32 query rows, whole rows at a time, all under way at once
+    {
+        uint4 v[32 / RPI];
+#pragma unroll
+        for (int i = 0; i < 32 / RPI; ++i) {
+            const int r = tile_row0 + warp * 32 + i * RPI + lane / LR;
+            const int tok = a.G == 1 ? r : r / a.G, head = a.G == 1 ? 0 : r - tok * a.G;
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < u.n_rows)
+                v[i] = __ldg(reinterpret_cast<const uint4 *>(a.q + u.b * a.qs[0] + (u.hk * a.G + head) * a.qs[1] +
+                                                             tok * a.qs[2] + (lane % LR) * 8));
+        }
+#pragma unroll
+        for (int i = 0; i < 32 / RPI; ++i) {
+            const uint32_t y[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            st_shared_v4(s_tile + swz<D>(warp * 32 + i * RPI + lane / LR, lane % LR), y);
+        }
     }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar.q_full());
-
+    fence_proxy_async_smem();  // before the block meets: Q is there for the tensor cores after it
+    block_meets();
+    if (*skip) return;
+    const uint32_t tmem = *tmem_slot;
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
     const uint32_t t_o = lane_base + tcol_o(x);
     const int r = tile_row0 + row;
@@ -831,13 +853,14 @@ __device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *s
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
-        if (a.n_split > 1) {
-            if (there) {
-                float4 *dst = reinterpret_cast<float4 *>(a.part_o + (u.split * part_rows + row_id(a, u, r)) * D + c * 32);
+        if (a.n_split > 1) {  // fp32 rows, 16-byte pieces turned by the row against bank conflicts
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    dst[q] = make_float4(__uint_as_float(o[4 * q]) * inv_l, __uint_as_float(o[4 * q + 1]) * inv_l,
-                                         __uint_as_float(o[4 * q + 2]) * inv_l, __uint_as_float(o[4 * q + 3]) * inv_l);
+            for (int q = 0; q < 8; ++q) {
+                const uint32_t y[4] = {__float_as_uint(__uint_as_float(o[4 * q]) * inv_l),
+                                       __float_as_uint(__uint_as_float(o[4 * q + 1]) * inv_l),
+                                       __float_as_uint(__uint_as_float(o[4 * q + 2]) * inv_l),
+                                       __float_as_uint(__uint_as_float(o[4 * q + 3]) * inv_l)};
+                st_shared_v4(s_part + row * D * 4 + (((c * 8 + q) ^ (row & 7)) << 4), y);
             }
         } else {
 #pragma unroll
@@ -854,14 +877,25 @@ __device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *s
         if (a.n_split > 1) a.part_lse[u.split * part_rows + row_id(a, u, r)] = lse2;
         else a.lse[row_id(a, u, r)] = lse2 * 0.69314718055994530942f;
     }
-    if (a.n_split > 1) return;
-    __syncwarp();  // a warp stores the 32 rows that its lanes have staged
+    __syncwarp();  // a warp stores the 32 rows that its lanes have staged, whole rows at a time
+    if (a.n_split > 1) {
+        constexpr int PL = D / 4, PR = 32 / PL;  // lanes per fp32 row, rows per access
+#pragma unroll 4
+        for (int i = 0; i < 32; i += PR) {
+            const int rr = warp * 32 + i + lane / PL, ch = lane % PL, ro = tile_row0 + rr;
+            if (ro < u.n_rows)
+                *reinterpret_cast<uint4 *>(a.part_o + (u.split * part_rows + row_id(a, u, ro)) * D + ch * 4) =
+                    *reinterpret_cast<const uint4 *>(smem + (s_part - sbase) + rr * D * 4 + ((ch ^ (rr & 7)) << 4));
+        }
+        return;
+    }
 #pragma unroll 4
     for (int i = 0; i < 32; i += RPI) {
         const int rr = warp * 32 + i + lane / LR, ch = lane % LR, ro = tile_row0 + rr;
+        const int tok = a.G == 1 ? ro : ro / a.G, head = a.G == 1 ? 0 : ro - tok * a.G;
         if (ro < u.n_rows)
-            *reinterpret_cast<uint4 *>(a.o + u.b * a.os[0] + (u.hk * a.G + ro % a.G) * a.os[1] + (ro / a.G) * a.os[2] +
-                                       ch * 8) = *reinterpret_cast<const uint4 *>(smem + (s_tile - sbase) + swz<D>(rr, ch));
+            *reinterpret_cast<uint4 *>(a.o + u.b * a.os[0] + (u.hk * a.G + head) * a.os[1] + tok * a.os[2] + ch * 8) =
+                *reinterpret_cast<const uint4 *>(smem + (s_tile - sbase) + swz<D>(rr, ch));
     }
 }
 
@@ -872,7 +906,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1) tile_attn_kernel(const __grid_c
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::SMEM_BAR + 240);
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + C::SMEM_BAR + 240);
     volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(smem + C::SMEM_BAR + 244);
     volatile int32_t *skip = reinterpret_cast<volatile int32_t *>(smem + C::SMEM_BAR + 248);
     const int warp = threadIdx.x >> 5;
@@ -885,7 +919,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1) tile_attn_kernel(const __grid_c
     const int ranges = n_ranges(a, all);
     if (u.split >= ranges) return skip_range(a, u, CT_ROWS);
     const int t0 = (int)((int64_t)all * u.split / ranges);
-    int n_tiles = (int)((int64_t)all * (u.split + 1) / ranges) - t0;
+    const int n_tiles = (int)((int64_t)all * (u.split + 1) / ranges) - t0;
     const bool has_b = u.row0 + BM < u.n_rows;
 
     if (threadIdx.x == 0) {
@@ -893,7 +927,6 @@ __global__ void __launch_bounds__(CT_THREADS, 1) tile_attn_kernel(const __grid_c
         for (int i = 0; i < CBars<D>::COUNT; ++i) mbar_init(sbase + C::SMEM_BAR + 8 * i, 1);
         for (int s = 0; s < C::NSK; ++s) mbar_init(bar.k_full(s), CT_K_WARPS);
         for (int s = 0; s < C::NSV; ++s) mbar_init(bar.v_full(s), CT_V_WARPS);
-        mbar_init(bar.q_full(), has_b ? CT_SOFTMAX_WARPS : CT_SOFTMAX_WARPS / 2);
         mbar_init(bar.p_full(0), BM / 32);
         mbar_init(bar.p_full(1), BM / 32);
         *abort_flag = 0;
@@ -902,84 +935,100 @@ __global__ void __launch_bounds__(CT_THREADS, 1) tile_attn_kernel(const __grid_c
         fence_mbar_init();
     }
     if (warp == CT_MMA_WARP) {
-        tmem_alloc(smem_u32(tmem_slot), TM_COLS);
+        tmem_alloc(sbase + C::SMEM_BAR + 240, TM_COLS);
         tmem_relinquish();
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
     const Ctl ctl{abort_flag, a.status, a.timeout_ns};
-    const bool skipped = *skip != 0;
-    if (skipped) n_tiles = 0;
 
     if (warp == CT_MMA_WARP) {
-        if (n_tiles > 0) {
-            if (has_b) chunk_mma<D, true>(sbase, tmem, n_tiles, ctl);
-            else chunk_mma<D, false>(sbase, tmem, n_tiles, ctl);
+        block_meets();
+        if (n_tiles > 0 && !*skip) {
+            if (has_b) chunk_mma<D, true>(sbase, *tmem_slot, n_tiles, ctl);
+            else chunk_mma<D, false>(sbase, *tmem_slot, n_tiles, ctl);
         }
+    } else if (warp >= CT_V_WARP) {
+        convert_role<D, false>(a, u, sbase, t0 * BN, seen, n_tiles, skip, ctl);
     } else if (warp >= CT_K_WARP) {
-        if (n_tiles > 0) {
-            if (warp < CT_V_WARP) convert_role<D, true>(a, u, sbase, t0 * BN, seen, n_tiles, ctl);
-            else convert_role<D, false>(a, u, sbase, t0 * BN, seen, n_tiles, ctl);
-        }
+        convert_role<D, true>(a, u, sbase, t0 * BN, seen, n_tiles, skip, ctl);
+    } else if (warp < 4 || has_b) {
+        chunk_softmax_role<D>(a, u, smem, sbase, tmem_slot, skip, warp >> 2, t0 * BN, n_tiles, !has_b, ctl);
     } else {
-        if (!skipped && (warp < 4 || has_b))
-            chunk_softmax_role<D>(a, u, smem, sbase, tmem, warp >> 2, t0 * BN, n_tiles, !has_b, ctl);
+        block_meets();
     }
 
     tc_fence_before();
     __syncthreads();
     if (warp == CT_MMA_WARP) {
         tc_fence_after();
-        tmem_dealloc(tmem, TM_COLS);
+        tmem_dealloc(*tmem_slot, TM_COLS);
     }
 }
 
 // ----------------------------------------------------------------- joining the ranges
 // O = sum_s w_s O_s, w_s = 2^(L_s - L), L = log2 sum_s 2^(L_s), over the key ranges of a row.
-// D / 8 lanes own a row, eight elements each.
+// A warp owns a row: its lanes hold the ranges' L_s (so their loads and the sum take one
+// round), then D / 32 elements each, several ranges' loads under way at a time.
+constexpr int JOIN_THREADS = 128;
+constexpr int MAX_SPLIT = 64;
+
 template <int D>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ ChunkArgs a)
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constant__ ChunkArgs a)
 {
     pdl_wait();  // the ranges are written by the kernel before
-    constexpr int G = D / 8;
+    constexpr int E = D / 32;  // elements a lane
     const int64_t rows = (int64_t)a.B * a.H * a.Lq;
-    const int64_t id = ((int64_t)blockIdx.x * 128 + threadIdx.x) / G;
+    const int64_t id = (int64_t)blockIdx.x * (JOIN_THREADS / 32) + (threadIdx.x >> 5);
     if (id >= rows) return;
-    const int e0 = (threadIdx.x % G) * 8;
-    const int64_t bh = id / a.Lq;
-    const int i = (int)(id - bh * a.Lq), b = (int)(bh / a.H), h = (int)(bh - (int64_t)b * a.H);
+    const int lane = threadIdx.x & 31;
+    const uint32_t bh = (uint32_t)id / (uint32_t)a.Lq;
+    const int i = (int)((uint32_t)id - bh * (uint32_t)a.Lq), b = (int)(bh / (uint32_t)a.H), h = (int)(bh - b * (uint32_t)a.H);
     if (a.q_lens && i >= __ldg(a.q_lens + b)) return;
-    float M = -INFINITY;
-    for (int s = 0; s < a.n_split; ++s) M = fmaxf(M, a.part_lse[s * rows + id]);
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, total = 0.f;
-    if (M != -INFINITY) {
-        for (int s = 0; s < a.n_split; ++s) {
-            const float ls = a.part_lse[s * rows + id];
-            if (ls == -INFINITY) continue;  // a range that was not there, or that the row does not see
-            const float w = ex2_approx(ls - M);
-            const float4 *src = reinterpret_cast<const float4 *>(a.part_o + (s * rows + id) * D + e0);
-            const float4 x = src[0], y = src[1];
-            total += w;
-            acc[0] = fmaf(w, x.x, acc[0]);
-            acc[1] = fmaf(w, x.y, acc[1]);
-            acc[2] = fmaf(w, x.z, acc[2]);
-            acc[3] = fmaf(w, x.w, acc[3]);
-            acc[4] = fmaf(w, y.x, acc[4]);
-            acc[5] = fmaf(w, y.y, acc[5]);
-            acc[6] = fmaf(w, y.z, acc[6]);
-            acc[7] = fmaf(w, y.w, acc[7]);
+    static_assert(MAX_SPLIT <= 64, "two ranges a lane");
+    const float l0 = lane < a.n_split ? a.part_lse[lane * rows + id] : -INFINITY;
+    const float l1 = lane + 32 < a.n_split ? a.part_lse[(lane + 32) * rows + id] : -INFINITY;
+    float M = fmaxf(l0, l1);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    // a range that was not there, or that the row does not see, has L_s = -inf and weight 0
+    const float w0 = l0 == -INFINITY ? 0.f : ex2_approx(l0 - M), w1 = l1 == -INFINITY ? 0.f : ex2_approx(l1 - M);
+    float total = w0 + w1;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    float acc[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) acc[j] = 0.f;
+    const float *src = a.part_o + id * D + lane * E;
+    for (int s0 = 0; s0 < a.n_split; s0 += 8) {
+        float x[8][E], w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int s = s0 + k;
+            w[k] = s < a.n_split ? __shfl_sync(0xffffffffu, s0 < 32 ? w0 : w1, s & 31) : 0.f;
+#pragma unroll
+            for (int j = 0; j < E; ++j) x[k][j] = 0.f;
+            if (w[k] != 0.f) {  // (the partial O of a range with weight 0 need not be there)
+                if (E == 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(src + s * rows * D);
+                    x[k][0] = v.x, x[k][1] = v.y, x[k][E - 2] = v.z, x[k][E - 1] = v.w;
+                } else {
+                    const float2 v = *reinterpret_cast<const float2 *>(src + s * rows * D);
+                    x[k][0] = v.x, x[k][1] = v.y;
+                }
+            }
         }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int j = 0; j < E; ++j) acc[j] = fmaf(w[k], x[k][j], acc[j]);
     }
     const float inv = total > 0.f ? 1.f / total : 0.f;
-    uint4 v;
-    v.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    v.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-    v.z = pack_bf16x2(acc[4] * inv, acc[5] * inv);
-    v.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
-    *reinterpret_cast<uint4 *>(a.o + b * a.os[0] + h * a.os[1] + i * a.os[2] + e0) = v;
-    if (e0 == 0) a.lse[id] = total > 0.f ? (M + log2f(total)) * 0.69314718055994530942f : -INFINITY;
+    uint16_t *dst = a.o + b * a.os[0] + h * a.os[1] + i * a.os[2] + lane * E;
+    if (E == 4)
+        *reinterpret_cast<uint2 *>(dst) =
+            make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[E - 2] * inv, acc[E - 1] * inv));
+    else
+        *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    if (lane == 0) a.lse[id] = total > 0.f ? (M + log2f(total)) * 0.69314718055994530942f : -INFINITY;
 }
 
 // ----------------------------------------------------------------- host side
@@ -1007,7 +1056,6 @@ struct Plan {
     int64_t ctas;
 };
 
-constexpr int MAX_SPLIT = 64;
 constexpr int TILE_MIN_ROWS = 17;
 
 Plan plan_of(const sfa_cache_attn_desc *d, const sfa_cache *c)
@@ -1136,9 +1184,9 @@ extern "C" sfa_status sfa_forward_cache(const sfa_cache_attn_desc *d, const sfa_
     }
     if (st != SFA_OK || p.n_split == 1) return st;
     cudaLaunchConfig_t cfg = {};
-    const int per_cta = 128 / (d->d / 8);
+    const int per_cta = JOIN_THREADS / 32;
     cfg.gridDim = dim3((unsigned)((rows + per_cta - 1) / per_cta));
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(JOIN_THREADS);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
