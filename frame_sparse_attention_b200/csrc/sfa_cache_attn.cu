@@ -734,7 +734,7 @@ __device__ __forceinline__ bool chunk_softmax_tile(uint32_t t_s, uint32_t t_o, i
                 tc_fence_after();
             }
             tmem_wait_ld_regs(ra);  // chunk 0 has arrived before the loads below
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 tmem_ld32(t_o + c * 32, rb);
                 tmem_wait_ld_regs(rb);
@@ -779,24 +779,17 @@ __device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *s
     // which nothing reads any more after the last product
     const uint32_t s_part = sbase + C::SMEM_Q + x * 2 * C::TILE_BYTES;
     static_assert(C::SMEM_V >= 4 * C::TILE_BYTES, "two tiles of fp32 rows end before the V slots");
-    // this warp's 32 query rows, whole rows at a time, all under way at once
-    {
-        uint4 v[32 / RPI];
-#pragma unroll
-        for (int i = 0; i < 32 / RPI; ++i) {
-            const int r = tile_row0 + warp * 32 + i * RPI + lane / LR;
-            const int tok = a.G == 1 ? r : r / a.G, head = a.G == 1 ? 0 : r - tok * a.G;
-            v[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < u.n_rows)
-                v[i] = __ldg(reinterpret_cast<const uint4 *>(a.q + u.b * a.qs[0] + (u.hk * a.G + head) * a.qs[1] +
-                                                             tok * a.qs[2] + (lane % LR) * 8));
-        }
-#pragma unroll
-        for (int i = 0; i < 32 / RPI; ++i) {
-            const uint32_t y[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            st_shared_v4(s_tile + swz<D>(warp * 32 + i * RPI + lane / LR, lane % LR), y);
-        }
+    // This warp's 32 query rows, whole rows at a time, all under way at once.  (What a CTA does
+    // once is kept in short loops: unrolled, it ran at the rate that its instructions came in.)
+#pragma unroll 1
+    for (int i = lane / LR; i < 32; i += RPI) {
+        const int rr = warp * 32 + i, r = tile_row0 + rr;
+        const int tok = a.G == 1 ? r : r / a.G, head = a.G == 1 ? 0 : r - tok * a.G;
+        const bool there = r < u.n_rows;
+        const uint16_t *src = a.q + u.b * a.qs[0] + (u.hk * a.G + head) * a.qs[1] + tok * a.qs[2] + (lane % LR) * 8;
+        cp_async16(s_tile + swz<D>(rr, lane % LR), there ? src : a.q, there);
     }
+    cp_async_wait_all();
     fence_proxy_async_smem();  // before the block meets: Q is there for the tensor cores after it
     block_meets();
     if (*skip) return;
@@ -843,7 +836,7 @@ __device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *s
     const bool there = r < u.n_rows;
     const int64_t part_rows = (int64_t)a.B * a.H * a.Lq;
     if (n_tiles > 0) tc_fence_after();
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         if (n_tiles > 0) {
@@ -880,7 +873,7 @@ __device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *s
     __syncwarp();  // a warp stores the 32 rows that its lanes have staged, whole rows at a time
     if (a.n_split > 1) {
         constexpr int PL = D / 4, PR = 32 / PL;  // lanes per fp32 row, rows per access
-#pragma unroll 4
+#pragma unroll 2
         for (int i = 0; i < 32; i += PR) {
             const int rr = warp * 32 + i + lane / PL, ch = lane % PL, ro = tile_row0 + rr;
             if (ro < u.n_rows)
@@ -889,7 +882,7 @@ __device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *s
         }
         return;
     }
-#pragma unroll 4
+#pragma unroll 2
     for (int i = 0; i < 32; i += RPI) {
         const int rr = warp * 32 + i + lane / LR, ch = lane % LR, ro = tile_row0 + rr;
         const int tok = a.G == 1 ? ro : ro / a.G, head = a.G == 1 ? 0 : ro - tok * a.G;
