@@ -160,6 +160,8 @@ __device__ __forceinline__ uint32_t scale_rest_bits(uint32_t scale_byte)
 {
     return (scale_byte > 134u ? scale_byte - 7u : 127u) << 7;
 }
-constexpr uint32_t SCALE_ONE_STEP = 134;  // scale bytes up to this need no second product
+// Scale bytes without their top bit (e <= 0, blocks of at most 448) need no second product, and
+// neither do those up to 134; the kernels look at the top bits.
+constexpr uint32_t SCALE_TOP_BITS = 0x80808080u;
 
 }  // namespace sfa

@@ -6,13 +6,8 @@
 // heads of a key head sharing its rows.
 //
 // Few query rows (rows_attn_kernel): every code is read once from HBM, converted and used for
-// at most 16 rows, so the floor is the cache's bytes.  The codes go from global memory to
-// registers in the lane layout of the m16n8k16 matrix instruction (its k index may be any
-// order of the elements as long as Q has the same), are turned into bf16 there (2.5
-// instructions per element) and never touch shared memory.  A warp owns 16 keys at a time;
-// the loads of the next keys are issued as soon as the registers are free; the key range is
-// cut over warps and CTAs so that all SMs stream, and the partial results are joined by their
-// log-sum-exp.
+// at most 16 rows, so the floor is the cache's bytes.
+#include <cuda.h>
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -108,9 +103,32 @@ __device__ __forceinline__ void skip_range(const ChunkArgs &a, const Unit &u, in
 }
 
 // ----------------------------------------------------------------- few query rows
+// Sixteen rows against the keys, with the m16n8k16 matrix instruction.  A warp owns every
+// fourth stretch of 16 keys of the CTA's range and streams them through a ring of its own in
+// shared memory, three stretches ahead of the one it works on: with the loads in registers
+// instead, one stretch ahead, the latency was not covered (130 us against HBM's 50 for one
+// token of 8 sequences over 16384 tokens; more registers a thread helped, more warps did not).
+// The codes are turned into bf16 in the lane layout of the instruction, whose k index may be
+// any order of the elements as long as Q has the same; the key range is cut over warps and
+// CTAs, and the partial results are joined by their log-sum-exp.
 constexpr int FR_WARPS = 4;
 constexpr int FR_ROWS = 16;              // the matrix instruction's rows
 constexpr int FR_KEYS = 16 * FR_WARPS;   // keys of one step of the CTA
+constexpr int FR_STAGES = 4;             // slots of a warp's ring
+constexpr int FR_CTAS = 3;               // CTAs an SM: 168 registers a thread
+
+template <int D>
+struct FCfg {
+    static constexpr int CODES = 16 * D;                // 16 rows of codes
+    static constexpr int SCALES = 16 * (D / CACHE_BLOCK);
+    static constexpr int RING = FR_WARPS * FR_STAGES * 2 * CODES;  // K, then V, of every slot
+    static constexpr int SMEM_SCALES = RING;
+    static constexpr int SMEM_BARS = SMEM_SCALES + FR_WARPS * FR_STAGES * 2 * SCALES;
+    static constexpr int SMEM_FLAGS = SMEM_BARS + FR_WARPS * FR_STAGES * 8;
+    static constexpr int SMEM_BYTES = SMEM_FLAGS + 16 + 1024;  // + alignment slack
+    static constexpr int O_PITCH = D + 4;               // floats of a row of a warp's O, in the ring's place
+    static_assert(FR_WARPS * FR_ROWS * O_PITCH * 4 <= RING, "O fits the ring");
+};
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1)
 {
@@ -129,12 +147,6 @@ __device__ __forceinline__ void codes_of_word(uint32_t w, uint32_t f, uint32_t &
     const uint32_t lo = (w << 4) & 0xf0f0f0f0u, hi = (w & 0x80808080u) | ((w >> 4) & 0x07070707u);
     p0 = mul_bf16x2(__byte_perm(lo, hi, 0x5140), f);
     p1 = mul_bf16x2(__byte_perm(lo, hi, 0x7362), f);
-}
-// code j of words lo and hi -> bf16 pair times f
-__device__ __forceinline__ uint32_t codes_of_two(uint32_t lo, uint32_t hi, int j, uint32_t f)
-{
-    const uint32_t sel = (uint32_t)j * 0x1111u + 0x4400u;
-    return mul_bf16x2(spread_codes(__byte_perm(lo, hi, sel)), f);
 }
 
 // compile-time answers for the code paths of large scales
@@ -156,21 +168,57 @@ struct ScaleWord<64> {
     typedef uint16_t type;
 };
 
-// Grid: (b, key head, row tile, key range), the key range fastest.  Lane (g = lane / 4,
-// t = lane % 4) holds, of 16 keys: of K the rows g and g + 8, elements c * 64 + 16 t .. + 15
-// (c = 0 .. D/64 - 1); of V the rows 2t, 2t + 1, 2t + 8, 2t + 9, elements g * D/8 .. + D/8 - 1.
-// Both reads touch whole 32-byte sectors.  Output column i of n-tile i' is then element
-// (its lane's column) * D/8 + i', so a lane ends up with D/4 consecutive elements of two rows.
+// byte offset of the 16-byte piece `ch` of row r in a slot: the order in which the tensor-map
+// copies store rows of 128 (64) bytes, under which the reads below meet no bank twice (V at
+// d = 64: twice)
 template <int D>
-__global__ void __launch_bounds__(FR_WARPS * 32, 4) rows_attn_kernel(const __grid_constant__ ChunkArgs a)
+__device__ __forceinline__ uint32_t slot_piece(int r, int ch)
 {
-    constexpr int KC = D / 64;          // 16-byte pieces of a K row per lane
+    return (uint32_t)(r * D + ((ch ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4));
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t addr)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds1(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+// Grid: (b, key head, row tile, key range), the key range fastest.  Lane (g = lane / 4,
+// t = lane % 4) holds, of 16 keys: of K the rows g and g + 8, elements t * D/4 .. + D/4 - 1
+// (at d = 128 one block); of V the rows 2t, 2t + 1, 2t + 8, 2t + 9, elements g * D/8 .. + D/8 - 1.
+// Output column i of n-tile i' is then element (its lane's column) * D/8 + i', so a lane ends up
+// with D/4 consecutive elements of two rows.
+// BULK (pages of a multiple of 16 rows, 16-byte aligned scales): a stretch of 16 keys is one
+// piece of memory, copied by one lane with two tensor-map boxes and two bulk copies; otherwise
+// the lanes look up a row each and copy 16-byte pieces.
+template <int D, bool BULK>
+__global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
+    rows_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ ChunkArgs a)
+{
+    using C = FCfg<D>;
+    constexpr int KS = D / 16;          // k-steps of S
+    constexpr int KP = D / 64;          // 16-byte pieces of a K row per lane
     constexpr int VW = D / 32;          // words of a V row per lane
     constexpr int NT = D / 8;           // n-tiles of the output
     typedef typename ScaleWord<D>::type scale_t;
-    __shared__ uint4 q_frag[D / 16][32];
-    __shared__ float o_sh[FR_WARPS][FR_ROWS][D + 4];
+    extern __shared__ uint8_t smem_raw[];
     __shared__ float ml_sh[FR_WARPS][FR_ROWS][2];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     if (a.n_split > 1) pdl_launch_dependents();  // the joining kernel's CTAs may take their places
@@ -182,26 +230,95 @@ __global__ void __launch_bounds__(FR_WARPS * 32, 4) rows_attn_kernel(const __gri
     const int steps = (seen + FR_KEYS - 1) / FR_KEYS;
     const int ranges = n_ranges(a, steps);
     if (u.split >= ranges) return skip_range(a, u, FR_ROWS);
+    const int s0 = (int)((int64_t)steps * u.split / ranges), s1 = (int)((int64_t)steps * (u.split + 1) / ranges);
+    // this warp's stretches: keys 64 (s0 + k) + 16 warp .. + 15, those that start before the end
+    const int key0 = s0 * FR_KEYS + warp * 16;
+    const int n = max(0, min(s1 - s0, (seen - key0 + FR_KEYS - 1) / FR_KEYS));
 
-    // Q in the A-operand layout of every k-step: rows g and g + 8, elements
-    // c * 64 + 16 t + 4 w + {0, 1} and {2, 3} of k-step 4 c + w
-    for (int x = tid; x < (D / 16) * 32; x += FR_WARPS * 32) {
-        const int ks = x >> 5, l = x & 31, e = (ks >> 2) * 64 + 16 * (l & 3) + 4 * (ks & 3);
-        uint2 v[2];
+    const uint32_t ring = sbase + warp * FR_STAGES * 2 * C::CODES;
+    const uint32_t scales = sbase + C::SMEM_SCALES + warp * FR_STAGES * 2 * C::SCALES;
+    const uint32_t bars = sbase + C::SMEM_BARS + warp * FR_STAGES * 8;
+    volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(smem + C::SMEM_FLAGS);
+    if (lane < FR_STAGES) mbar_init(bars + 8 * lane, BULK ? 1 : 32);
+    if (tid == 0) *abort_flag = 0;
+    fence_mbar_init();
+    __syncthreads();
+    const Ctl ctl{abort_flag, a.status, a.timeout_ns};
+
+    const int32_t *table = a.cache.table + u.b * a.cache.ts0 + u.hk * a.cache.ts1;
+    CachePlace place;  // of the next stretch to copy (BULK: its first row; else lane l's row is l mod 16)
+    auto look_up = [&](int k) {
+        const int j = key0 + k * FR_KEYS + (BULK ? 0 : lane & 15);
+        place.open(a.cache, table, j, k < n && j < seen);
+    };
+    uint32_t pending = 0u;  // !BULK: the scales that the stretch before is still to get
+    auto put_scales = [&](int k) {  // lanes 0-15: of K's rows, 16-31: of V's
+        const uint32_t at = scales + (k % FR_STAGES) * 2 * C::SCALES + lane * (C::SCALES / 16);
+        if (D == 128) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(pending) : "memory");
+        else asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)pending) : "memory");
+    };
+    auto copy = [&](int k) {  // stretch k into its slot
+        if (!BULK && k > 0 && k <= n) put_scales(k - 1);
+        if (k >= n) return;
+        const int s = k % FR_STAGES;
+        const uint32_t slot = ring + s * 2 * C::CODES, sc = scales + s * 2 * C::SCALES, bar = bars + 8 * s;
+        const int r = place.row(a.cache, u.hk, a.status), row = max(r, 0);
+        if (BULK) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, 2 * C::CODES + 2 * C::SCALES);
+                tma_load_2d(slot, &tm_k, bar, 0, row);
+                tma_load_2d(slot + C::CODES, &tm_v, bar, 0, row);
+                bulk_load(sc, a.cache.k_scale + (int64_t)row * (D / CACHE_BLOCK), C::SCALES, bar);
+                bulk_load(sc + C::SCALES, a.cache.v_scale + (int64_t)row * (D / CACHE_BLOCK), C::SCALES, bar);
+            }
+        } else {
+            constexpr int PR = D / 16, RPI = 32 / PR;  // pieces of a row, rows per access of the warp
+#pragma unroll
+            for (int i = 0; i < 16 / RPI; ++i) {
+                const int rr = i * RPI + lane / PR, ch = lane % PR;
+                const int src = __shfl_sync(0xffffffffu, r, rr);
+                const int64_t at = (int64_t)max(src, 0) * D + ch * 16;
+                cp_async16(slot + slot_piece<D>(rr, ch), a.cache.k + at, src >= 0);
+                cp_async16(slot + C::CODES + slot_piece<D>(rr, ch), a.cache.v + at, src >= 0);
+            }
+            cp_async_arrive(bar);
+            pending = (uint32_t)__ldg(reinterpret_cast<const scale_t *>(lane < 16 ? a.cache.k_scale : a.cache.v_scale) + row);
+        }
+    };
+    look_up(0);
+    for (int k = 0; k < FR_STAGES - 1; ++k) {
+        copy(k);
+        look_up(k + 1);
+    }
+
+    // Q in the A-operand layout of every k-step: rows g and g + 8, elements t * D/4 + 4 ks
+    // + {0, 1} and {2, 3}
+    uint4 qf[KS];
+    {
+        const uint16_t *src[2];
+        bool on[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int r = u.row0 + (l >> 2) + 8 * s;
-            v[s] = make_uint2(0u, 0u);
-            if (r < u.n_rows)
-                v[s] = *reinterpret_cast<const uint2 *>(a.q + u.b * a.qs[0] + (u.hk * a.G + r % a.G) * a.qs[1] +
-                                                        (r / a.G) * a.qs[2] + e);
+            const int r = u.row0 + g + 8 * s;
+            on[s] = r < u.n_rows;
+            const int tok = on[s] ? r / a.G : 0, head = on[s] ? r - tok * a.G : 0;
+            src[s] = a.q + u.b * a.qs[0] + (u.hk * a.G + head) * a.qs[1] + tok * a.qs[2] + t * (D / 4);
         }
-        q_frag[ks][l] = make_uint4(v[0].x, v[1].x, v[0].y, v[1].y);
+#pragma unroll
+        for (int ks = 0; ks < KS; ks += 2) {  // 8 consecutive elements: two k-steps
+            uint4 v[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                v[s] = on[s] ? __ldg(reinterpret_cast<const uint4 *>(src[s] + 4 * ks)) : make_uint4(0u, 0u, 0u, 0u);
+            qf[ks] = make_uint4(v[0].x, v[1].x, v[0].y, v[1].y);
+            qf[ks + 1] = make_uint4(v[0].z, v[1].z, v[0].w, v[1].w);
+        }
     }
-    __syncthreads();
-
-    const int lim0 = row_limit(a, u, u.row0 + g), lim1 = row_limit(a, u, u.row0 + g + 8);
-    const int s0 = (int)((int64_t)steps * u.split / ranges), s1 = (int)((int64_t)steps * (u.split + 1) / ranges);
+    // keys that rows g and g + 8 see; rows that are not there see all of them
+    const int r0 = u.row0 + g, r1 = r0 + 8;
+    const int lim0 = r0 < u.n_rows ? row_limit(a, u, r0) : seen, lim1 = r1 < u.n_rows ? row_limit(a, u, r1) : seen;
+    const int lim_all = __reduce_min_sync(0xffffffffu, min(lim0, lim1));  // what every row sees
+    const float sl2 = a.scale_log2;
 
     float o[NT][4];
 #pragma unroll
@@ -210,101 +327,47 @@ __global__ void __launch_bounds__(FR_WARPS * 32, 4) rows_attn_kernel(const __gri
         for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // of rows g and g + 8
 
-    // place of key (16 of them: lanes 0-15, repeated in 16-31) of step s
-    const int32_t *table = a.cache.table + u.b * a.cache.ts0 + u.hk * a.cache.ts1;
-    CachePlace place;
-    auto look_up = [&](int s) {
-        const int j = s * FR_KEYS + warp * 16 + (lane & 15);
-        place.open(a.cache, table, j, s < s1 && j < seen);
-    };
-    uint4 kr[2][KC];
-    uint32_t vr[4][VW], kf[2], vf[4];  // codes and scales of this lane's K and V rows
-    uint32_t absent = 0u;              // bits 0, 1: of K, bits 2 .. 5: of V, the row is not there
-    const scale_t *k_scale = reinterpret_cast<const scale_t *>(a.cache.k_scale);
-    const scale_t *v_scale = reinterpret_cast<const scale_t *>(a.cache.v_scale);
-    // Rows that are not there read row 0 of the pool and get the scale byte 0, which makes any
-    // code a finite number: their keys are masked and their probabilities 0.
-    auto load_k = [&](int rows) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            int r = __shfl_sync(0xffffffffu, rows, g + 8 * s);
-            absent = (absent & ~(1u << s)) | (r < 0 ? 1u << s : 0u);
-            r = max(r, 0);
-            kf[s] = (uint32_t)__ldg(k_scale + r);
-#pragma unroll
-            for (int c = 0; c < KC; ++c) kr[s][c] = load_codes16(a.cache.k + (int64_t)r * D + c * 64 + t * 16);
-        }
-    };
-    auto load_v = [&](int rows) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            int r = __shfl_sync(0xffffffffu, rows, 2 * t + (s & 1) + (s >> 1) * 8);
-            absent = (absent & ~(4u << s)) | (r < 0 ? 4u << s : 0u);
-            r = max(r, 0);
-            vf[s] = (uint32_t)__ldg(v_scale + r);
-            const uint8_t *p = a.cache.v + (int64_t)r * D + g * NT;
-            if (D == 128) {
-                const uint4 x = load_codes16(p);
-                vr[s][0] = x.x, vr[s][1] = x.y, vr[s][VW - 2] = x.z, vr[s][VW - 1] = x.w;
-            } else {
-                const uint2 x = load_codes8(p);
-                vr[s][0] = x.x, vr[s][1] = x.y;
-            }
-        }
-    };
-
-    look_up(s0);
-    int rows = place.row(a.cache, u.hk, a.status);
-    load_k(rows);
-    load_v(rows);
-    look_up(s0 + 1);
-    auto step = [&](auto two, int st, int rows_next) {
+    int k = 0;
+    // TWO: a block of these rows has e > 0, whose 2^(120 + e) may pass bf16's range
+    auto stretch = [&](auto two, uint32_t slot, const uint32_t (&kb)[2], const uint32_t (&vb)[4]) {
         // ---- S = Q K^T, keys 8 s + 2 t + {0, 1} of rows g, g + 8
         float sc[2][4];
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int s = 0; s < 2; ++s) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) sc[s][j] = 0.f;
+            const uint32_t f = scale_bits(kb[s]) * 0x10001u, r2 = scale_rest_bits(kb[s]) * 0x10001u;
 #pragma unroll
-        for (int c = 0; c < KC; ++c) {
-            uint32_t f[2], r2[2];
+            for (int c = 0; c < KP; ++c) {
+                const uint4 kr = lds16(slot + slot_piece<D>(g + 8 * s, KP * t + c));
+                const uint32_t w[4] = {kr.x, kr.y, kr.z, kr.w};
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const uint32_t byte = (kf[s] >> (8 * (2 * c + (t >> 1)))) & 0xffu;
-                f[s] = scale_bits(byte) * 0x10001u;
-                r2[s] = scale_rest_bits(byte) * 0x10001u;
-            }
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const uint4 qf = q_frag[4 * c + w][lane];
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const uint32_t kw = w == 0 ? kr[s][c].x : w == 1 ? kr[s][c].y : w == 2 ? kr[s][c].z : kr[s][c].w;
+                for (int i = 0; i < 4; ++i) {
                     uint32_t b0, b1;
-                    codes_of_word(kw, f[s], b0, b1);
+                    codes_of_word(w[i], f, b0, b1);
                     if (decltype(two)::value) {
-                        b0 = mul_bf16x2(b0, r2[s]);
-                        b1 = mul_bf16x2(b1, r2[s]);
+                        b0 = mul_bf16x2(b0, r2);
+                        b1 = mul_bf16x2(b1, r2);
                     }
-                    mma_16816(sc[s], qf, b0, b1);
+                    mma_16816(sc[s], qf[4 * c + i], b0, b1);
                 }
             }
         }
-        load_k(rows_next);
 
-        // ---- softmax of this warp's 16 keys (log2 units, scale folded in)
-        const int key = st * FR_KEYS + warp * 16 + 2 * t;
-        float x0 = -INFINITY, x1 = -INFINITY;
+        // ---- softmax of these keys (log2 units, the scale folded into the exponent's FMA)
+        const int key = key0 + k * FR_KEYS;
+        if (key + 16 > lim_all) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                sc[s][j] = key + 8 * s + j < lim0 ? sc[s][j] * a.scale_log2 : -INFINITY;
-                sc[s][2 + j] = key + 8 * s + j < lim1 ? sc[s][2 + j] * a.scale_log2 : -INFINITY;
-                x0 = fmaxf(x0, sc[s][j]);
-                x1 = fmaxf(x1, sc[s][2 + j]);
-            }
+                for (int j = 0; j < 2; ++j) {
+                    const int x = key + 8 * s + 2 * t + j;
+                    sc[s][j] = x < lim0 ? sc[s][j] : -INFINITY;
+                    sc[s][2 + j] = x < lim1 ? sc[s][2 + j] : -INFINITY;
+                }
         }
+        float x0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1])) * sl2;
+        float x1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3])) * sl2;
         // the running max is kept while no score exceeds it by 2^8; -inf (nothing seen) is
         // always replaced
         if (__any_sync(0xffffffffu, x0 > m0 + 8.f || x1 > m1 + 8.f)) {
@@ -327,16 +390,16 @@ __global__ void __launch_bounds__(FR_WARPS * 32, 4) rows_attn_kernel(const __gri
                 o[i][3] *= c1;
             }
         }
-        const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
+        const float z0 = m0 == -INFINITY ? 0.f : -m0, z1 = m1 == -INFINITY ? 0.f : -m1;
         uint4 p;
         {
             float e[8];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                e[4 * s] = ex2_approx(sc[s][0] - z0);
-                e[4 * s + 1] = ex2_approx(sc[s][1] - z0);
-                e[4 * s + 2] = ex2_approx(sc[s][2] - z1);
-                e[4 * s + 3] = ex2_approx(sc[s][3] - z1);
+                e[4 * s] = ex2_approx(fmaf(sc[s][0], sl2, z0));
+                e[4 * s + 1] = ex2_approx(fmaf(sc[s][1], sl2, z0));
+                e[4 * s + 2] = ex2_approx(fmaf(sc[s][2], sl2, z1));
+                e[4 * s + 3] = ex2_approx(fmaf(sc[s][3], sl2, z1));
                 l0 += e[4 * s] + e[4 * s + 1];
                 l1 += e[4 * s + 2] + e[4 * s + 3];
             }
@@ -346,41 +409,71 @@ __global__ void __launch_bounds__(FR_WARPS * 32, 4) rows_attn_kernel(const __gri
             p.w = pack_bf16x2(e[6], e[7]);
         }
 
-        // ---- O += P V
-        const int blk = (g * NT) / CACHE_BLOCK * 8;
-        uint32_t f01 = scale_bits((vf[0] >> blk) & 0xffu) | (scale_bits((vf[1] >> blk) & 0xffu) << 16);
-        uint32_t f23 = scale_bits((vf[2] >> blk) & 0xffu) | (scale_bits((vf[3] >> blk) & 0xffu) << 16);
-        uint32_t r01 = scale_rest_bits((vf[0] >> blk) & 0xffu) | (scale_rest_bits((vf[1] >> blk) & 0xffu) << 16);
-        uint32_t r23 = scale_rest_bits((vf[2] >> blk) & 0xffu) | (scale_rest_bits((vf[3] >> blk) & 0xffu) << 16);
+        // ---- O += P V: the codes of two keys are dealt into pairs, then converted like K's
+        uint32_t f[2], r2[2], v[4][VW];  // keys 2t, 2t + 1 and 2t + 8, 2t + 9
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            uint32_t b0 = codes_of_two(vr[0][i / 4], vr[1][i / 4], i % 4, f01);
-            uint32_t b1 = codes_of_two(vr[2][i / 4], vr[3][i / 4], i % 4, f23);
-            if (decltype(two)::value) {
-                b0 = mul_bf16x2(b0, r01);
-                b1 = mul_bf16x2(b1, r23);
+        for (int s = 0; s < 2; ++s) {
+            f[s] = scale_bits(vb[2 * s]) | (scale_bits(vb[2 * s + 1]) << 16);
+            r2[s] = scale_rest_bits(vb[2 * s]) | (scale_rest_bits(vb[2 * s + 1]) << 16);
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int r = 2 * t + (s & 1) + (s >> 1) * 8;
+            if (D == 128) {
+                const uint4 x = lds16(slot + C::CODES + slot_piece<D>(r, g));
+                v[s][0] = x.x, v[s][1] = x.y, v[s][VW - 2] = x.z, v[s][VW - 1] = x.w;
+            } else {
+                const uint2 x = lds8(slot + C::CODES + slot_piece<D>(r, g >> 1) + (g & 1) * 8);
+                v[s][0] = x.x, v[s][1] = x.y;
             }
-            mma_16816(o[i], p, b0, b1);
         }
-        load_v(rows_next);
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+            uint32_t b[2][4];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                codes_of_word(__byte_perm(v[2 * s][w], v[2 * s + 1][w], 0x5140), f[s], b[s][0], b[s][1]);
+                codes_of_word(__byte_perm(v[2 * s][w], v[2 * s + 1][w], 0x7362), f[s], b[s][2], b[s][3]);
+                if (decltype(two)::value) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) b[s][i] = mul_bf16x2(b[s][i], r2[s]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma_16816(o[4 * w + i], p, b[0][i], b[1][i]);
+        }
     };
-    for (int st = s0; st < s1; ++st) {
-        const int rows_next = place.row(a.cache, u.hk, a.status);
-        look_up(st + 2);
-        if (absent) {
+    for (; k < n; ++k) {
+        copy(k + FR_STAGES - 1);  // into the slot that the stretch before has left
+        look_up(k + FR_STAGES);
+        const int s = k % FR_STAGES;
+        if (!__all_sync(0xffffffffu, wait_bar(bars + 8 * s, (k / FR_STAGES) & 1, ctl))) break;
+        __syncwarp();  // (!BULK: the scales stored by other lanes)
+        const uint32_t slot = ring + s * 2 * C::CODES, sc = scales + s * 2 * C::SCALES;
+        // scale bytes of this lane's blocks; a row that is not there gets 0, under which any code
+        // is a finite number (its key is masked, its probability 0)
+        uint32_t kb[2], vb[4];
+        constexpr int SB = D / CACHE_BLOCK;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) kf[s] = (absent >> s) & 1u ? 0u : kf[s];
+        for (int i = 0; i < 2; ++i) kb[i] = lds1(sc + (g + 8 * i) * SB + (D == 128 ? t : t >> 1));
 #pragma unroll
-            for (int s = 0; s < 4; ++s) vf[s] = (absent >> (2 + s)) & 1u ? 0u : vf[s];
+        for (int i = 0; i < 4; ++i)
+            vb[i] = lds1(sc + C::SCALES + (2 * t + (i & 1) + (i >> 1) * 8) * SB + g * NT / CACHE_BLOCK);
+        const int left = seen - (key0 + k * FR_KEYS);
+        if (left < 16) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) kb[i] = g + 8 * i < left ? kb[i] : 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vb[i] = 2 * t + (i & 1) + (i >> 1) * 8 < left ? vb[i] : 0u;
         }
-        // 2^e beyond bf16's range in one step (e > 7, values of 57344 and more) takes a second product
-        bool two = false;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) two |= __vcmpgtu4(kf[s], 0x01010101u * SCALE_ONE_STEP) != 0u;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) two |= __vcmpgtu4(vf[s], 0x01010101u * SCALE_ONE_STEP) != 0u;
-        if (__any_sync(0xffffffffu, two)) step(Yes{}, st, rows_next);
-        else step(No{}, st, rows_next);
+        const uint32_t top = kb[0] | kb[1] | vb[0] | vb[1] | vb[2] | vb[3];
+        if (__any_sync(0xffffffffu, (top & SCALE_TOP_BITS) != 0u)) stretch(Yes{}, slot, kb, vb);
+        else stretch(No{}, slot, kb, vb);
+        __syncwarp();  // the slot has been read
+    }
+    if (*abort_flag) {  // a wait ran out: the copies still on their way land before the CTA ends
+        for (int j = k; j < min(n, k + FR_STAGES); ++j) wait_drain(bars + 8 * (j % FR_STAGES), (j / FR_STAGES) & 1);
+        cp_async_wait_all();
     }
 
     // ---- join the warps: every warp's O against the common max, then the sum of four
@@ -389,6 +482,9 @@ __global__ void __launch_bounds__(FR_WARPS * 32, 4) rows_attn_kernel(const __gri
         l0 += __shfl_xor_sync(0xffffffffu, l0, d);
         l1 += __shfl_xor_sync(0xffffffffu, l1, d);
     }
+    __syncthreads();  // every ring has been read: O takes their place
+    if (*abort_flag) return;
+    float *o_sh = reinterpret_cast<float *>(smem) + warp * FR_ROWS * C::O_PITCH;
     if (t == 0) {
         ml_sh[warp][g][0] = m0;
         ml_sh[warp][g][1] = l0;
@@ -398,10 +494,10 @@ __global__ void __launch_bounds__(FR_WARPS * 32, 4) rows_attn_kernel(const __gri
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         // columns 2t and 2t + 1 of n-tile i are elements 2t * NT + i and (2t + 1) * NT + i
-        o_sh[warp][g][2 * t * NT + i] = o[i][0];
-        o_sh[warp][g][(2 * t + 1) * NT + i] = o[i][1];
-        o_sh[warp][g + 8][2 * t * NT + i] = o[i][2];
-        o_sh[warp][g + 8][(2 * t + 1) * NT + i] = o[i][3];
+        o_sh[g * C::O_PITCH + 2 * t * NT + i] = o[i][0];
+        o_sh[g * C::O_PITCH + (2 * t + 1) * NT + i] = o[i][1];
+        o_sh[(g + 8) * C::O_PITCH + 2 * t * NT + i] = o[i][2];
+        o_sh[(g + 8) * C::O_PITCH + (2 * t + 1) * NT + i] = o[i][3];
     }
     __syncthreads();
     const int64_t part_rows = (int64_t)a.B * a.H * a.Lq;
@@ -415,21 +511,22 @@ __global__ void __launch_bounds__(FR_WARPS * 32, 4) rows_attn_kernel(const __gri
         for (int w = 0; w < FR_WARPS; ++w) {
             const float mw = ml_sh[w][r][0];
             const float c = mw == -INFINITY ? 0.f : ex2_approx(mw - M);
+            const float *src = reinterpret_cast<const float *>(smem) + (w * FR_ROWS + r) * C::O_PITCH + e0;
             l += c * ml_sh[w][r][1];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] = fmaf(c, o_sh[w][r][e0 + j], acc[j]);
+            for (int j = 0; j < 8; ++j) acc[j] = fmaf(c, src[j], acc[j]);
         }
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const float lse2 = l > 0.f ? M + log2f(l) : -INFINITY;
-        const int h = u.hk * a.G + row % a.G, i = row / a.G;
         const int64_t id = row_id(a, u, row);
         if (a.n_split == 1) {
+            const int tok = row / a.G, h = u.hk * a.G + (row - tok * a.G);
             uint4 v;
             v.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
             v.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
             v.z = pack_bf16x2(acc[4] * inv, acc[5] * inv);
             v.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
-            *reinterpret_cast<uint4 *>(a.o + u.b * a.os[0] + h * a.os[1] + i * a.os[2] + e0) = v;
+            *reinterpret_cast<uint4 *>(a.o + u.b * a.os[0] + h * a.os[1] + tok * a.os[2] + e0) = v;
             if (e0 == 0) a.lse[id] = lse2 * 0.69314718055994530942f;
         } else {
             float4 *dst = reinterpret_cast<float4 *>(a.part_o + ((int64_t)u.split * part_rows + id) * D + e0);
@@ -612,10 +709,10 @@ __device__ void convert_role(const ChunkArgs &a, const Unit &u, uint32_t sbase, 
     block_meets();
     if (*skip) return;
     for (int j = 0; j < n_tiles; ++j) {
-        bool two = false;
+        uint32_t top = sw[0];
 #pragma unroll
-        for (int k = 0; k < LK; ++k) two |= __vcmpgtu4(sw[k], 0x01010101u * SCALE_ONE_STEP) != 0u;
-        const bool go = __any_sync(0xffffffffu, two) ? one_tile(Yes{}, j) : one_tile(No{}, j);
+        for (int k = 1; k < LK; ++k) top |= sw[k];
+        const bool go = __any_sync(0xffffffffu, (top & SCALE_TOP_BITS) != 0u) ? one_tile(Yes{}, j) : one_tile(No{}, j);
         if (!go) return;
         look_up(j + 2);
     }
@@ -1064,7 +1161,7 @@ Plan plan_of(const sfa_cache_attn_desc *d, const sfa_cache *c)
     const int64_t steps = std::max<int64_t>(1, (kv + step_keys - 1) / step_keys);
     // Modelled as waves of equal ranges: a range costs its steps and a fixed start and end,
     // and the joining kernel the partial results' bytes (in steps of a CTA's share).
-    const double slots = (double)attn_sms() * (p.tiles ? 1 : 4);
+    const double slots = (double)attn_sms() * (p.tiles ? 1 : FR_CTAS);
     const double fixed = p.tiles ? 4.0 : 6.0;
     const double step_us = p.tiles ? 2.4 : 1.6;
     const double join_us = (double)d->B * d->H * d->Lq * (d->d + 1) * 4.0 / 5.0e6;
@@ -1091,6 +1188,45 @@ sfa_status launch_tiles(const ChunkArgs &a, unsigned grid, cudaStream_t s)
         return SFA_ERR_CUDA;
     tile_attn_kernel<D><<<grid, CT_THREADS, CCfg<D>::SMEM_BYTES, s>>>(a);
     return launch_status();
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                             const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// A pool's codes as rows of d bytes, copied 16 rows at a time.
+bool encode_pool(CUtensorMap *m, const void *codes, int d, int64_t rows)
+{
+    EncodeFn fn = reinterpret_cast<EncodeFn>(tensor_map_encoder());
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)d};
+    const cuuint32_t box[2] = {(cuuint32_t)d, 16}, ones[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(codes), dims, strides, box, ones,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool BULK>
+sfa_status launch_rows_attn(const ChunkArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, unsigned grid, cudaStream_t s)
+{
+    if (cudaFuncSetAttribute(rows_attn_kernel<D, BULK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             FCfg<D>::SMEM_BYTES) != cudaSuccess)
+        return SFA_ERR_CUDA;
+    rows_attn_kernel<D, BULK><<<grid, FR_WARPS * 32, FCfg<D>::SMEM_BYTES, s>>>(tk, tv, a);
+    return launch_status();
+}
+
+sfa_status launch_few_rows(const ChunkArgs &a, const sfa_cache *c, unsigned grid, cudaStream_t s)
+{
+    CUtensorMap tk = {}, tv = {};
+    const bool bulk = c->page_len % 16 == 0 && reinterpret_cast<uintptr_t>(c->k_scale) % 16 == 0 &&
+                      reinterpret_cast<uintptr_t>(c->v_scale) % 16 == 0;
+    if (bulk) {
+        const int64_t rows = (int64_t)c->n_pages * c->heads * c->page_len;
+        if (!encode_pool(&tk, c->k, c->d, rows) || !encode_pool(&tv, c->v, c->d, rows)) return SFA_ERR_CUDA;
+        return c->d == 128 ? launch_rows_attn<128, true>(a, tk, tv, grid, s) : launch_rows_attn<64, true>(a, tk, tv, grid, s);
+    }
+    return c->d == 128 ? launch_rows_attn<128, false>(a, tk, tv, grid, s) : launch_rows_attn<64, false>(a, tk, tv, grid, s);
 }
 
 size_t part_bytes(const sfa_cache_attn_desc *d, int n_split)
@@ -1171,9 +1307,7 @@ extern "C" sfa_status sfa_forward_cache(const sfa_cache_attn_desc *d, const sfa_
     if (p.tiles) {
         st = d->d == 128 ? launch_tiles<128>(a, grid, s) : launch_tiles<64>(a, grid, s);
     } else {
-        if (d->d == 128) rows_attn_kernel<128><<<grid, FR_WARPS * 32, 0, s>>>(a);
-        else rows_attn_kernel<64><<<grid, FR_WARPS * 32, 0, s>>>(a);
-        st = launch_status();
+        st = launch_few_rows(a, cache, grid, s);
     }
     if (st != SFA_OK || p.n_split == 1) return st;
     cudaLaunchConfig_t cfg = {};

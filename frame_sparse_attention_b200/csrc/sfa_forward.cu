@@ -1175,6 +1175,9 @@ sfa_status check_buffers(const sfa_attn_desc *d, const void *q, const void *k, c
 }
 
 }  // namespace
+
+void *tensor_map_encoder() { return reinterpret_cast<void *>(encode_fn()); }
+
 }  // namespace sfa
 
 using namespace sfa;

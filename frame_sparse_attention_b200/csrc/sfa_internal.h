@@ -27,4 +27,7 @@ sfa_status launch_lse_combine(int64_t rows, int S, int d, int H, int64_t Lq, con
                               const float *lse_part, void *o, const int64_t *o_stride, float *lse, cudaStream_t s,
                               int S1 = 0, void *o1 = nullptr, float *lse1 = nullptr);
 
+// cuTensorMapEncodeTiled, looked up once per process (sfa_forward.cu); NULL where the driver has none.
+void *tensor_map_encoder();
+
 }  // namespace sfa

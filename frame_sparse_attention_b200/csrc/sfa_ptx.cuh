@@ -187,6 +187,20 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&v)[
                  : "memory");
 }
 
+// `bytes` (a multiple of 16, both ends 16-byte aligned) from global to shared memory, counted by `bar`
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// one arrival on `bar` when this thread's cp.async copies so far have landed (the barrier's count includes it)
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // 16 bytes from global to shared memory, asynchronously (completion through cp_async_wait_all);
 // zeros, and nothing read, where there is nothing to copy
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool there)
