@@ -160,6 +160,12 @@ __device__ __forceinline__ uint32_t scale_rest_bits(uint32_t scale_byte)
 {
     return (scale_byte > 134u ? scale_byte - 7u : 127u) << 7;
 }
+// The same, twice (both halves of a word) or of two scale bytes, for bytes below 135
+__device__ __forceinline__ uint32_t scale_pair(uint32_t byte) { return byte * 0x00800080u + 0x3c003c00u; }
+__device__ __forceinline__ uint32_t scale_pair(uint32_t lo, uint32_t hi)
+{
+    return hi * 0x00800000u + (lo * 0x80u + 0x3c003c00u);
+}
 // Scale bytes without their top bit (e <= 0, blocks of at most 448) need no second product, and
 // neither do those up to 134; the kernels look at the top bits.
 constexpr uint32_t SCALE_TOP_BITS = 0x80808080u;

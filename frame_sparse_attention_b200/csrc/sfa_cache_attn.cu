@@ -104,23 +104,25 @@ __device__ __forceinline__ void skip_range(const ChunkArgs &a, const Unit &u, in
 
 // ----------------------------------------------------------------- few query rows
 // Sixteen rows against the keys, with the m16n8k16 matrix instruction.  A warp owns every
-// fourth stretch of 16 keys of the CTA's range and streams them through a ring of its own in
-// shared memory, three stretches ahead of the one it works on: with the loads in registers
-// instead, one stretch ahead, the latency was not covered (130 us against HBM's 50 for one
-// token of 8 sequences over 16384 tokens; more registers a thread helped, more warps did not).
-// The codes are turned into bf16 in the lane layout of the instruction, whose k index may be
-// any order of the elements as long as Q has the same; the key range is cut over warps and
-// CTAs, and the partial results are joined by their log-sum-exp.
+// fourth stretch of 32 keys of the CTA's range and streams them through a ring of its own in
+// shared memory, so that the next stretch is on its way while it works on one: with the loads
+// in registers the latency was not covered (130 us against HBM's 50 for one token of 8
+// sequences over 16384 tokens).  The codes are turned into bf16 in the lane layout of the
+// instruction, whose k index may be any order of the elements as long as Q has the same; the
+// key range is cut over warps and CTAs, and the partial results are joined by their log-sum-exp.
+// What bounds it is the conversion: about 2.5 instructions a code, on a pipe that takes one
+// every two cycles, next to 32 matrix instructions of 8 cycles for 16 keys.
 constexpr int FR_WARPS = 4;
 constexpr int FR_ROWS = 16;              // the matrix instruction's rows
-constexpr int FR_KEYS = 16 * FR_WARPS;   // keys of one step of the CTA
-constexpr int FR_STAGES = 4;             // slots of a warp's ring
+constexpr int FR_STRETCH = 32;           // keys that a warp works on at a time
+constexpr int FR_KEYS = FR_STRETCH * FR_WARPS;  // keys of one step of the CTA
+constexpr int FR_STAGES = 2;             // slots of a warp's ring
 constexpr int FR_CTAS = 3;               // CTAs an SM: 168 registers a thread
 
 template <int D>
 struct FCfg {
-    static constexpr int CODES = 16 * D;                // 16 rows of codes
-    static constexpr int SCALES = 16 * (D / CACHE_BLOCK);
+    static constexpr int CODES = FR_STRETCH * D;                // a stretch's codes
+    static constexpr int SCALES = FR_STRETCH * (D / CACHE_BLOCK);
     static constexpr int RING = FR_WARPS * FR_STAGES * 2 * CODES;  // K, then V, of every slot
     static constexpr int SMEM_SCALES = RING;
     static constexpr int SMEM_BARS = SMEM_SCALES + FR_WARPS * FR_STAGES * 2 * SCALES;
@@ -132,7 +134,7 @@ struct FCfg {
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1)
 {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -197,13 +199,13 @@ __device__ __forceinline__ uint32_t lds1(uint32_t addr)
 }
 
 // Grid: (b, key head, row tile, key range), the key range fastest.  Lane (g = lane / 4,
-// t = lane % 4) holds, of 16 keys: of K the rows g and g + 8, elements t * D/4 .. + D/4 - 1
-// (at d = 128 one block); of V the rows 2t, 2t + 1, 2t + 8, 2t + 9, elements g * D/8 .. + D/8 - 1.
+// t = lane % 4) holds, of 32 keys: of K the rows g + 8 i, elements t * D/4 .. + D/4 - 1 (at
+// d = 128 one block); of V the rows 16 h + 2t + {0, 1, 8, 9}, elements g * D/8 .. + D/8 - 1.
 // Output column i of n-tile i' is then element (its lane's column) * D/8 + i', so a lane ends up
 // with D/4 consecutive elements of two rows.
-// BULK (pages of a multiple of 16 rows, 16-byte aligned scales): a stretch of 16 keys is one
-// piece of memory, copied by one lane with two tensor-map boxes and two bulk copies; otherwise
-// the lanes look up a row each and copy 16-byte pieces.
+// BULK (pages of a multiple of 16 rows, 16-byte aligned scales): 16 keys are one piece of
+// memory, and lanes 0 and 1 copy a half each with two tensor-map boxes and two bulk copies;
+// otherwise the lanes look up a row each and copy 16-byte pieces.
 template <int D, bool BULK>
 __global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
     rows_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -231,8 +233,8 @@ __global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
     const int ranges = n_ranges(a, steps);
     if (u.split >= ranges) return skip_range(a, u, FR_ROWS);
     const int s0 = (int)((int64_t)steps * u.split / ranges), s1 = (int)((int64_t)steps * (u.split + 1) / ranges);
-    // this warp's stretches: keys 64 (s0 + k) + 16 warp .. + 15, those that start before the end
-    const int key0 = s0 * FR_KEYS + warp * 16;
+    // this warp's stretches: keys FR_KEYS (s0 + k) + 32 warp .. + 31, those that start before the end
+    const int key0 = s0 * FR_KEYS + warp * FR_STRETCH;
     const int n = max(0, min(s1 - s0, (seen - key0 + FR_KEYS - 1) / FR_KEYS));
 
     const uint32_t ring = sbase + warp * FR_STAGES * 2 * C::CODES;
@@ -246,35 +248,42 @@ __global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
     const Ctl ctl{abort_flag, a.status, a.timeout_ns};
 
     const int32_t *table = a.cache.table + u.b * a.cache.ts0 + u.hk * a.cache.ts1;
-    CachePlace place;  // of the next stretch to copy (BULK: its first row; else lane l's row is l mod 16)
+    CachePlace place;  // of the next stretch to copy (BULK: the first row of half lane & 1; else row `lane`)
     auto look_up = [&](int k) {
-        const int j = key0 + k * FR_KEYS + (BULK ? 0 : lane & 15);
+        const int j = key0 + k * FR_KEYS + (BULK ? (lane & 1) * 16 : lane);
         place.open(a.cache, table, j, k < n && j < seen);
     };
-    uint32_t pending = 0u;  // !BULK: the scales that the stretch before is still to get
-    auto put_scales = [&](int k) {  // lanes 0-15: of K's rows, 16-31: of V's
-        const uint32_t at = scales + (k % FR_STAGES) * 2 * C::SCALES + lane * (C::SCALES / 16);
-        if (D == 128) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(pending) : "memory");
-        else asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)pending) : "memory");
+    uint32_t pend_k = 0u, pend_v = 0u;  // !BULK: the scales that the stretch before is still to get
+    auto put_scales = [&](int k) {
+        const uint32_t at = scales + (k % FR_STAGES) * 2 * C::SCALES + lane * (D / CACHE_BLOCK);
+        if (D == 128) {
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(pend_k) : "memory");
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + C::SCALES), "r"(pend_v) : "memory");
+        } else {
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)pend_k) : "memory");
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + C::SCALES), "h"((uint16_t)pend_v) : "memory");
+        }
     };
     auto copy = [&](int k) {  // stretch k into its slot
-        if (!BULK && k > 0 && k <= n) put_scales(k - 1);
         if (k >= n) return;
         const int s = k % FR_STAGES;
         const uint32_t slot = ring + s * 2 * C::CODES, sc = scales + s * 2 * C::SCALES, bar = bars + 8 * s;
         const int r = place.row(a.cache, u.hk, a.status), row = max(r, 0);
         if (BULK) {
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar, 2 * C::CODES + 2 * C::SCALES);
-                tma_load_2d(slot, &tm_k, bar, 0, row);
-                tma_load_2d(slot + C::CODES, &tm_v, bar, 0, row);
-                bulk_load(sc, a.cache.k_scale + (int64_t)row * (D / CACHE_BLOCK), C::SCALES, bar);
-                bulk_load(sc + C::SCALES, a.cache.v_scale + (int64_t)row * (D / CACHE_BLOCK), C::SCALES, bar);
+            if (lane == 0)
+                mbar_arrive_expect_tx(bar, (C::CODES + C::SCALES) * (key0 + k * FR_KEYS + 16 < seen ? 2 : 1));
+            __syncwarp();
+            if (lane < 2 && place.wanted) {
+                constexpr int HC = C::CODES / 2, HS = C::SCALES / 2;
+                tma_load_2d(slot + lane * HC, &tm_k, bar, 0, row);
+                tma_load_2d(slot + C::CODES + lane * HC, &tm_v, bar, 0, row);
+                bulk_load(sc + lane * HS, a.cache.k_scale + (int64_t)row * (D / CACHE_BLOCK), HS, bar);
+                bulk_load(sc + C::SCALES + lane * HS, a.cache.v_scale + (int64_t)row * (D / CACHE_BLOCK), HS, bar);
             }
         } else {
             constexpr int PR = D / 16, RPI = 32 / PR;  // pieces of a row, rows per access of the warp
 #pragma unroll
-            for (int i = 0; i < 16 / RPI; ++i) {
+            for (int i = 0; i < FR_STRETCH / RPI; ++i) {
                 const int rr = i * RPI + lane / PR, ch = lane % PR;
                 const int src = __shfl_sync(0xffffffffu, r, rr);
                 const int64_t at = (int64_t)max(src, 0) * D + ch * 16;
@@ -282,7 +291,8 @@ __global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
                 cp_async16(slot + C::CODES + slot_piece<D>(rr, ch), a.cache.v + at, src >= 0);
             }
             cp_async_arrive(bar);
-            pending = (uint32_t)__ldg(reinterpret_cast<const scale_t *>(lane < 16 ? a.cache.k_scale : a.cache.v_scale) + row);
+            pend_k = (uint32_t)__ldg(reinterpret_cast<const scale_t *>(a.cache.k_scale) + row);
+            pend_v = (uint32_t)__ldg(reinterpret_cast<const scale_t *>(a.cache.v_scale) + row);
         }
     };
     look_up(0);
@@ -329,45 +339,59 @@ __global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
 
     int k = 0;
     // TWO: a block of these rows has e > 0, whose 2^(120 + e) may pass bf16's range
-    auto stretch = [&](auto two, uint32_t slot, const uint32_t (&kb)[2], const uint32_t (&vb)[4]) {
-        // ---- S = Q K^T, keys 8 s + 2 t + {0, 1} of rows g, g + 8
-        float sc[2][4];
+    auto stretch = [&](auto two, uint32_t slot, const uint32_t (&kb)[4], const uint32_t (&vb)[8]) {
+        constexpr bool TWO = decltype(two)::value;
+        // ---- S = Q K^T, keys 8 i + 2 t + {0, 1} of rows g, g + 8
+        float sc[4][4];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sc[s][j] = 0.f;
-            const uint32_t f = scale_bits(kb[s]) * 0x10001u, r2 = scale_rest_bits(kb[s]) * 0x10001u;
+            for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
+        uint32_t kf[4], kf2[4];
 #pragma unroll
-            for (int c = 0; c < KP; ++c) {
-                const uint4 kr = lds16(slot + slot_piece<D>(g + 8 * s, KP * t + c));
-                const uint32_t w[4] = {kr.x, kr.y, kr.z, kr.w};
+        for (int i = 0; i < 4; ++i) {
+            kf[i] = TWO ? scale_bits(kb[i]) * 0x10001u : scale_pair(kb[i]);
+            kf2[i] = scale_rest_bits(kb[i]) * 0x10001u;
+        }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+        for (int c = 0; c < KP; ++c) {
+            uint4 kr[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) kr[i] = lds16(slot + slot_piece<D>(g + 8 * i, KP * t + c));
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // four sums in turn
                     uint32_t b0, b1;
-                    codes_of_word(w[i], f, b0, b1);
-                    if (decltype(two)::value) {
-                        b0 = mul_bf16x2(b0, r2);
-                        b1 = mul_bf16x2(b1, r2);
+                    codes_of_word(w == 0 ? kr[i].x : w == 1 ? kr[i].y : w == 2 ? kr[i].z : kr[i].w, kf[i], b0, b1);
+                    if (TWO) {
+                        b0 = mul_bf16x2(b0, kf2[i]);
+                        b1 = mul_bf16x2(b1, kf2[i]);
                     }
-                    mma_16816(sc[s], qf[4 * c + i], b0, b1);
+                    mma_16816(sc[i], qf[4 * c + w], b0, b1);
                 }
-            }
         }
 
         // ---- softmax of these keys (log2 units, the scale folded into the exponent's FMA)
         const int key = key0 + k * FR_KEYS;
-        if (key + 16 > lim_all) {
+        if (key + FR_STRETCH > lim_all) {
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const int x = key + 8 * s + 2 * t + j;
-                    sc[s][j] = x < lim0 ? sc[s][j] : -INFINITY;
-                    sc[s][2 + j] = x < lim1 ? sc[s][2 + j] : -INFINITY;
+                    const int x = key + 8 * i + 2 * t + j;
+                    sc[i][j] = x < lim0 ? sc[i][j] : -INFINITY;
+                    sc[i][2 + j] = x < lim1 ? sc[i][2 + j] : -INFINITY;
                 }
         }
-        float x0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1])) * sl2;
-        float x1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3])) * sl2;
+        float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x0 = fmax3(x0, sc[i][0], sc[i][1]);
+            x1 = fmax3(x1, sc[i][2], sc[i][3]);
+        }
+        x0 *= sl2;
+        x1 *= sl2;
         // the running max is kept while no score exceeds it by 2^8; -inf (nothing seen) is
         // always replaced
         if (__any_sync(0xffffffffu, x0 > m0 + 8.f || x1 > m1 + 8.f)) {
@@ -391,60 +415,68 @@ __global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
             }
         }
         const float z0 = m0 == -INFINITY ? 0.f : -m0, z1 = m1 == -INFINITY ? 0.f : -m1;
-        uint4 p;
-        {
+        uint4 p[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
             float e[8];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                e[4 * s] = ex2_approx(fmaf(sc[s][0], sl2, z0));
-                e[4 * s + 1] = ex2_approx(fmaf(sc[s][1], sl2, z0));
-                e[4 * s + 2] = ex2_approx(fmaf(sc[s][2], sl2, z1));
-                e[4 * s + 3] = ex2_approx(fmaf(sc[s][3], sl2, z1));
+                const float(&x)[4] = sc[2 * h + s];
+                e[4 * s] = ex2_approx(fmaf(x[0], sl2, z0));
+                e[4 * s + 1] = ex2_approx(fmaf(x[1], sl2, z0));
+                e[4 * s + 2] = ex2_approx(fmaf(x[2], sl2, z1));
+                e[4 * s + 3] = ex2_approx(fmaf(x[3], sl2, z1));
                 l0 += e[4 * s] + e[4 * s + 1];
                 l1 += e[4 * s + 2] + e[4 * s + 3];
             }
-            p.x = pack_bf16x2(e[0], e[1]);
-            p.y = pack_bf16x2(e[2], e[3]);
-            p.z = pack_bf16x2(e[4], e[5]);
-            p.w = pack_bf16x2(e[6], e[7]);
+            p[h].x = pack_bf16x2(e[0], e[1]);
+            p[h].y = pack_bf16x2(e[2], e[3]);
+            p[h].z = pack_bf16x2(e[4], e[5]);
+            p[h].w = pack_bf16x2(e[6], e[7]);
         }
 
-        // ---- O += P V: the codes of two keys are dealt into pairs, then converted like K's
-        uint32_t f[2], r2[2], v[4][VW];  // keys 2t, 2t + 1 and 2t + 8, 2t + 9
+        // ---- O += P V, 16 keys at a time: the codes of two keys are dealt into pairs, then
+        // converted like K's
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            f[s] = scale_bits(vb[2 * s]) | (scale_bits(vb[2 * s + 1]) << 16);
-            r2[s] = scale_rest_bits(vb[2 * s]) | (scale_rest_bits(vb[2 * s + 1]) << 16);
-        }
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int r = 2 * t + (s & 1) + (s >> 1) * 8;
-            if (D == 128) {
-                const uint4 x = lds16(slot + C::CODES + slot_piece<D>(r, g));
-                v[s][0] = x.x, v[s][1] = x.y, v[s][VW - 2] = x.z, v[s][VW - 1] = x.w;
-            } else {
-                const uint2 x = lds8(slot + C::CODES + slot_piece<D>(r, g >> 1) + (g & 1) * 8);
-                v[s][0] = x.x, v[s][1] = x.y;
-            }
-        }
-#pragma unroll
-        for (int w = 0; w < VW; ++w) {
-            uint32_t b[2][4];
+        for (int h = 0; h < 2; ++h) {
+            uint32_t f[2], f2[2], v[4][VW];  // keys 2t, 2t + 1 and 2t + 8, 2t + 9
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                codes_of_word(__byte_perm(v[2 * s][w], v[2 * s + 1][w], 0x5140), f[s], b[s][0], b[s][1]);
-                codes_of_word(__byte_perm(v[2 * s][w], v[2 * s + 1][w], 0x7362), f[s], b[s][2], b[s][3]);
-                if (decltype(two)::value) {
+                const uint32_t ba = vb[4 * h + 2 * s], bb = vb[4 * h + 2 * s + 1];
+                f[s] = TWO ? scale_bits(ba) | (scale_bits(bb) << 16) : scale_pair(ba, bb);
+                f2[s] = scale_rest_bits(ba) | (scale_rest_bits(bb) << 16);
+            }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) b[s][i] = mul_bf16x2(b[s][i], r2[s]);
+            for (int s = 0; s < 4; ++s) {
+                const int r = 16 * h + 2 * t + (s & 1) + (s >> 1) * 8;
+                if (D == 128) {
+                    const uint4 x = lds16(slot + C::CODES + slot_piece<D>(r, g));
+                    v[s][0] = x.x, v[s][1] = x.y, v[s][VW - 2] = x.z, v[s][VW - 1] = x.w;
+                } else {
+                    const uint2 x = lds8(slot + C::CODES + slot_piece<D>(r, g >> 1) + (g & 1) * 8);
+                    v[s][0] = x.x, v[s][1] = x.y;
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma_16816(o[4 * w + i], p, b[0][i], b[1][i]);
+            for (int w = 0; w < VW; ++w) {
+                uint32_t b[2][4];
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    codes_of_word(__byte_perm(v[2 * s][w], v[2 * s + 1][w], 0x5140), f[s], b[s][0], b[s][1]);
+                    codes_of_word(__byte_perm(v[2 * s][w], v[2 * s + 1][w], 0x7362), f[s], b[s][2], b[s][3]);
+                    if (TWO) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) b[s][i] = mul_bf16x2(b[s][i], f2[s]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mma_16816(o[4 * w + i], p[h], b[0][i], b[1][i]);
+            }
         }
     };
     for (; k < n; ++k) {
-        copy(k + FR_STAGES - 1);  // into the slot that the stretch before has left
+        if (!BULK) put_scales(k);  // (asked for a stretch ago)
+        copy(k + FR_STAGES - 1);   // into the slot that the stretch before has left
         look_up(k + FR_STAGES);
         const int s = k % FR_STAGES;
         if (!__all_sync(0xffffffffu, wait_bar(bars + 8 * s, (k / FR_STAGES) & 1, ctl))) break;
@@ -452,21 +484,23 @@ __global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
         const uint32_t slot = ring + s * 2 * C::CODES, sc = scales + s * 2 * C::SCALES;
         // scale bytes of this lane's blocks; a row that is not there gets 0, under which any code
         // is a finite number (its key is masked, its probability 0)
-        uint32_t kb[2], vb[4];
+        uint32_t kb[4], vb[8];
         constexpr int SB = D / CACHE_BLOCK;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) kb[i] = lds1(sc + (g + 8 * i) * SB + (D == 128 ? t : t >> 1));
+        for (int i = 0; i < 4; ++i) kb[i] = lds1(sc + (g + 8 * i) * SB + (D == 128 ? t : t >> 1));
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 8; ++i)
             vb[i] = lds1(sc + C::SCALES + (2 * t + (i & 1) + (i >> 1) * 8) * SB + g * NT / CACHE_BLOCK);
         const int left = seen - (key0 + k * FR_KEYS);
-        if (left < 16) {
+        if (left < FR_STRETCH) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) kb[i] = g + 8 * i < left ? kb[i] : 0u;
+            for (int i = 0; i < 4; ++i) kb[i] = g + 8 * i < left ? kb[i] : 0u;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) vb[i] = 2 * t + (i & 1) + (i >> 1) * 8 < left ? vb[i] : 0u;
+            for (int i = 0; i < 8; ++i) vb[i] = 2 * t + (i & 1) + (i >> 1) * 8 < left ? vb[i] : 0u;
         }
-        const uint32_t top = kb[0] | kb[1] | vb[0] | vb[1] | vb[2] | vb[3];
+        uint32_t top = kb[0] | kb[1] | kb[2] | kb[3];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top |= vb[i];
         if (__any_sync(0xffffffffu, (top & SCALE_TOP_BITS) != 0u)) stretch(Yes{}, slot, kb, vb);
         else stretch(No{}, slot, kb, vb);
         __syncwarp();  // the slot has been read
@@ -657,7 +691,8 @@ __device__ void convert_role(const ChunkArgs &a, const Unit &u, uint32_t sbase, 
     uint32_t present = 0u;  // `there` of the tile that is being converted
     // codes of x[i] -> eight bf16 pairs; TWO: exponents above 7 somewhere in the warp's rows
     auto convert = [&](auto two, int i, uint32_t byte, uint32_t (&y)[8]) {
-        const uint32_t f = (present >> i) & 1u ? scale_bits(byte) * 0x10001u : 0u;
+        const uint32_t some = decltype(two)::value ? scale_bits(byte) * 0x10001u : scale_pair(byte);
+        const uint32_t f = (present >> i) & 1u ? some : 0u;
         codes_of_word(x[i].x, f, y[0], y[1]);
         codes_of_word(x[i].y, f, y[2], y[3]);
         codes_of_word(x[i].z, f, y[4], y[5]);
