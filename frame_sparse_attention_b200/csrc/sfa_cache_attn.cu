@@ -43,6 +43,14 @@ struct ChunkArgs {
     uint32_t debug_flags;
 };
 
+// A row keeps a running maximum m that later scores have outgrown while their probabilities
+// 2^(s - m) stay below 2^GROWTH.  They are floating numbers (bf16 for the product with V, fp32
+// in the sums), so their precision does not depend on m; what limits the growth is overflow, of
+// O from values beyond 2^(127 - GROWTH).  A small limit costs time instead: with 2^8, keys of
+// uneven norm sent the rows of the streaming chunk through the rescaling often enough to take
+// 764 us instead of 571.
+constexpr float GROWTH = 24.f;
+
 // What a CTA works on: rows [row0, row0 + tile) of (b, hk), row r being token r / G of query
 // head hk * G + r % G, and its share of the keys those rows see.
 struct Unit {
@@ -392,9 +400,8 @@ __global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
         }
         x0 *= sl2;
         x1 *= sl2;
-        // the running max is kept while no score exceeds it by 2^8; -inf (nothing seen) is
-        // always replaced
-        if (__any_sync(0xffffffffu, x0 > m0 + 8.f || x1 > m1 + 8.f)) {
+        // a maximum of -inf (nothing seen) is always replaced
+        if (__any_sync(0xffffffffu, x0 > m0 + GROWTH || x1 > m1 + GROWTH)) {
 #pragma unroll
             for (int d = 1; d < 4; d <<= 1) {
                 x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
@@ -822,75 +829,103 @@ done:
 }
 
 template <bool MASK>
-__device__ __forceinline__ void hide_columns(int c, int nv, uint32_t (&r)[32])
+__device__ __forceinline__ void hide_columns(int nv, uint32_t (&r)[32])
 {
-    if (MASK && c * 32 + 32 > nv) {
+    if (MASK && nv < 32) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            if (c * 32 + i >= nv) r[i] = __float_as_uint(-INFINITY);
+            if (i >= nv) r[i] = __float_as_uint(-INFINITY);
+    }
+}
+
+// A chunk of 32 columns has outgrown the running max m of some row: the row takes the chunk's
+// maximum, and what stands against the old one shrinks by alpha (by 2^-19 or more, or all of it is
+// 0): O, the row sum and the probabilities of the tile's chunks before, whose second rounding
+// to bf16 is 2^-8 of that little.
+template <int D>
+__device__ __noinline__ void outgrown(uint32_t t_s, uint32_t t_o, int chunks, bool has_o, float alpha)
+{
+    uint32_t r[16];
+    tmem_wait_st();  // the probabilities just stored are read again
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+        tmem_ld16_wait(t_s + c * 16, r);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            r[i] = pack_bf16x2(__uint_as_float(r[i] << 16) * alpha, __uint_as_float(r[i] & 0xffff0000u) * alpha);
+        tmem_st16(t_s + c * 16, r);
+    }
+    if (!has_o) return;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 16) {
+        tmem_ld16_wait(t_o + c, r);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+        tmem_st16(t_o + c, r);
     }
 }
 
 // One key tile of the online softmax for this thread's row (thread = TMEM lane) that sees the
-// columns [0, nv) of it (MASK; all of them otherwise): the row's maximum first, then
-// P = exp2(S * scale * log2e - m) as bf16 over the columns that S has been read from.  m is
-// kept while it is at most 2^8 behind the maximum, else O and the row sum are rescaled; it
-// stays -inf, and the row's probabilities 0, until the row has seen a key.  P V of the key
-// tile before is complete: S of this one came after it, or (one-tile units) pv_done says so.
+// columns [0, nv) of it (MASK; all of them otherwise), 32 columns at a time:
+// P = exp2(S * scale * log2e - m) as bf16 over the columns that S has been read from.  The first
+// tile takes its row maximum before; later a row keeps m until a chunk's probabilities sum to
+// more than 2^GROWTH (one above it, or enough of them).  m is -inf, and the row's
+// probabilities are 0, until the row has seen a key.  P V of the key tile before is complete: S of
+// this one came after it, or (one-tile units) pv_done says so.
 template <int D, bool MASK>
 __device__ __forceinline__ bool chunk_softmax_tile(uint32_t t_s, uint32_t t_o, int nv, float sl2, float &m_used, float &l,
                                                    int j, uint32_t pv_done, const Ctl &ctl)
 {
     uint32_t ra[32], rb[32];  // the load of chunk c + 1 is in flight while chunk c is used
-    float mx = -INFINITY;
-    tmem_ld32(t_s, ra);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t(&cur)[32] = (c & 1) ? rb : ra;
-        uint32_t(&nxt)[32] = (c & 1) ? ra : rb;
-        tmem_wait_ld_regs(cur);
-        tmem_ld32(t_s + ((c + 1) & 3) * 32, nxt);  // after the last one: chunk 0 again, for its exponentials
-        hide_columns<MASK>(c, nv, cur);
-        mx = fmaxf(mx, max32(cur));
+    if (j == 0) {
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+            tmem_ld32(t_s + c * 32, ra);
+            tmem_wait_ld_regs(ra);
+            hide_columns<MASK>(nv - c * 32, ra);
+            mx = fmaxf(mx, max32(ra));
+        }
+        m_used = mx * sl2;
     }
-    const float m_cand = mx * sl2;
-    const bool grow = m_cand > m_used + 8.f;
-    if (__any_sync(0xffffffffu, grow)) {
-        const float m_new = grow ? m_cand : m_used;
-        const float alpha = !grow ? 1.f : m_used == -INFINITY ? 0.f : ex2_approx(m_used - m_new);
-        l *= alpha;
-        m_used = m_new;
-        if (j > 0) {
-            if (pv_done) {
-                if (!__all_sync(0xffffffffu, wait_bar(pv_done, (j - 1) & 1, ctl))) return false;
+    float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+    constexpr float limit = (float)(1 << (int)GROWTH);
+    bool ok = true;
+    auto chunk = [&](int c, uint32_t(&cur)[32], uint32_t(&nxt)[32], bool more) {
+        tmem_wait_ld_regs(cur);
+        if (more) tmem_ld32(t_s + (c + 1) * 32, nxt);
+        hide_columns<MASK>(nv - c * 32, cur);
+        uint32_t pk[16];
+        Acc8 acc;
+        exp_chunk(cur, sl2, neg_m, pk, acc);
+        float lt = sum8(acc);
+        const bool grow = lt > limit || (MASK && m_used == -INFINITY && c * 32 < nv);
+        if (__any_sync(0xffffffffu, grow)) {
+            const float m_new = grow ? fmaxf(m_used, max32(cur) * sl2) : m_used;
+            const float alpha = m_used == -INFINITY ? 0.f : ex2_approx(m_used - m_new);
+            if (j > 0 && pv_done) {
+                ok = ok && __all_sync(0xffffffffu, wait_bar(pv_done, (j - 1) & 1, ctl));
                 tc_fence_after();
             }
-            tmem_wait_ld_regs(ra);  // chunk 0 has arrived before the loads below
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                tmem_ld32(t_o + c * 32, rb);
-                tmem_wait_ld_regs(rb);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) rb[i] = __float_as_uint(__uint_as_float(rb[i]) * alpha);
-                tmem_st32(t_o + c * 32, rb);
-            }
+            if (more) tmem_wait_ld_regs(nxt);
+            outgrown<D>(t_s, t_o, c, j > 0, alpha);
+            l *= alpha;
+            m_used = m_new;
+            neg_m = m_used == -INFINITY ? 0.f : -m_used;
+            Acc8 again;
+            exp_chunk(cur, sl2, neg_m, pk, again);
+            lt = sum8(again);
         }
-    }
-    const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-    Acc8 acc;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t(&cur)[32] = (c & 1) ? rb : ra;
-        uint32_t(&nxt)[32] = (c & 1) ? ra : rb;
-        tmem_wait_ld_regs(cur);
-        if (c < 3) tmem_ld32(t_s + (c + 1) * 32, nxt);
-        hide_columns<MASK>(c, nv, cur);
-        uint32_t pk[16];
-        exp_chunk(cur, sl2, neg_m, pk, acc);
+        l += lt;
         tmem_st16(t_s + c * 16, pk);
+    };
+    tmem_ld32(t_s, ra);
+#pragma unroll 1
+    for (int c = 0; c < 4; c += 2) {
+        chunk(c, ra, rb, true);
+        chunk(c + 1, rb, ra, c == 0);
     }
-    l += sum8(acc);
-    return true;
+    return ok;
 }
 
 // Queries, softmax and epilogue of query tile x, one thread per row.
@@ -1194,19 +1229,24 @@ Plan plan_of(const sfa_cache_attn_desc *d, const sfa_cache *c)
     int64_t kv = (int64_t)c->table_len * c->page_len;
     if (d->max_kv > 0 && d->max_kv < kv) kv = d->max_kv;
     const int64_t steps = std::max<int64_t>(1, (kv + step_keys - 1) / step_keys);
-    // Modelled as waves of equal ranges: a range costs its steps and a fixed start and end,
-    // and the joining kernel the partial results' bytes (in steps of a CTA's share).
+    // The number of ranges per unit, by the steps that the launch takes: a range takes its own
+    // steps and a fixed start and end, and the join of k ranges a little.  The lengths are on
+    // the device, so the mean of two cases is taken: all caches as long as the bound (whole
+    // waves of equal ranges), and lengths spread between half of it and all of it (three
+    // quarters of the ranges, which then even out but for the last one's end).  Measured, one
+    // token, 96 units of 128 steps, k = 3, 6, 9, 12, 18: 103, 106, 100, 105, 107 us at one
+    // length and 98, 107, 85, 91, 88 at uneven ones; 32 units: k = 9, 13, 18: 43, 41, 49.
     const double slots = (double)attn_sms() * (p.tiles ? 1 : FR_CTAS);
-    const double fixed = p.tiles ? 4.0 : 6.0;
-    const double step_us = p.tiles ? 2.4 : 1.6;
-    const double join_us = (double)d->B * d->H * d->Lq * (d->d + 1) * 4.0 / 5.0e6;
+    const double fixed = p.tiles ? 5.0 : 2.0;
     double best = 1e300;
     p.n_split = 1;
     for (int64_t k = 1; k <= MAX_SPLIT && k <= steps; ++k) {
-        const double len = (double)((steps + k - 1) / k);
-        const double us = std::ceil(units * k / slots) * (len + fixed) * step_us + (k > 1 ? 3.0 + (k + 1) * join_us : 0.0);
-        if (us < best) {
-            best = us;
+        const double piece = (double)((steps + k - 1) / k) + fixed, waves = units * k / slots;
+        const double even = std::ceil(waves) * piece;
+        const double uneven = waves <= 1.0 ? piece : (0.75 * waves + 0.5) * piece;
+        const double cost = 0.5 * (even + uneven) + (k > 1 ? 1.5 + 0.05 * k : 0.0);
+        if (cost < best) {
+            best = cost;
             p.n_split = (int)k;
         }
     }
