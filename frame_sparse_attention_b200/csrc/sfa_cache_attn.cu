@@ -48,7 +48,7 @@ struct ChunkArgs {
 // in the sums), so their precision does not depend on m; what limits the growth is overflow, of
 // O from values beyond 2^(127 - GROWTH).  A small limit costs time instead: with 2^8, keys of
 // uneven norm sent the rows of the streaming chunk through the rescaling often enough to take
-// 764 us instead of 571.
+// 764 us instead of 568.
 constexpr float GROWTH = 24.f;
 
 // What a CTA works on: rows [row0, row0 + tile) of (b, hk), row r being token r / G of query
@@ -581,7 +581,8 @@ __global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
 // ----------------------------------------------------------------- many query rows
 // Units of two 128-row query tiles A and B against 128-key tiles, on the tensor cores:
 //   S_A(0) S_B(0) | P V_A(j) S_A(j+1) | P V_B(j) S_B(j+1) | ...
-// While the softmax of one query tile runs, the tensor cores work on the other.  A unit with
+// (at d = 64, where P has columns of its own, S_x(j+1) before P V_x(j)).  While the softmax of
+// one query tile runs, the tensor cores work on the other.  A unit with
 // one query tile has both tiles' S buffers to itself and keeps S one key tile ahead:
 //   S(0) S(1) | P V(j) S(j+2) | ...
 // Seven warps load the codes of the K and V tiles into registers, look up the pages of the
@@ -592,7 +593,7 @@ __global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
 // operands there takes all of its bandwidth, and the converted tiles have to get in as well
 // (with P in shared memory, as in the frame-list kernel, a key tile took 5600 cycles, 2200 of
 // them in the issue of 11 loads behind blocked stores).  So P stays in tensor memory, in the
-// columns of the S that it comes from, as the first operand of P V.
+// columns of the S that it comes from or beside it, as the first operand of P V.
 // warps 0-3: softmax of query tile A, 4-7: of B
 constexpr int CT_K_WARP = 8;              // 8-11: codes of K to bf16
 constexpr int CT_V_WARP = 12;             // 12-14: of V
@@ -600,6 +601,14 @@ constexpr int CT_MMA_WARP = 15;
 constexpr int CT_K_WARPS = CT_V_WARP - CT_K_WARP, CT_V_WARPS = CT_MMA_WARP - CT_V_WARP;
 constexpr int CT_THREADS = 512;           // four warps to a scheduler: 128 registers a thread
 constexpr int CT_ROWS = 2 * BM;
+
+// Tensor-memory columns of P of buffer x: at d = 64 its own, beside O; at d = 128, where S and O
+// take all 512, those of the S that it comes from.
+template <int D>
+__host__ __device__ constexpr uint32_t tcol_p(int x)
+{
+    return D == 64 ? tcol_o(x) + 64 : tcol_s(x);
+}
 
 template <int D>
 struct CCfg {
@@ -626,7 +635,8 @@ struct CBars {
     __device__ uint32_t o_final() const { return base + 8 * (2 * NSK + 2 * NSV + 4); }  // after the last P V
     __device__ uint32_t pv_done() const { return base + 8 * (2 * NSK + 2 * NSV + 5); }  // one-tile units: a P V
     __device__ uint32_t drain() const { return base + 8 * (2 * NSK + 2 * NSV + 6); }
-    static constexpr int COUNT = 2 * NSK + 2 * NSV + 7;
+    __device__ uint32_t pv_x(int x) const { return base + 8 * (2 * NSK + 2 * NSV + 7 + x); }  // d = 64: P V of tile x
+    static constexpr int COUNT = 2 * NSK + 2 * NSV + 9;
     static_assert(8 * COUNT <= 160, "mbarriers end before the flags at +160");
 };
 
@@ -805,15 +815,21 @@ __device__ void chunk_mma(uint32_t sbase, uint32_t tmem, int n_tiles, const Ctl 
         for (int i = 0; i < (PAIR ? 2 : 1); ++i) {
             const int x = PAIR ? i : j & 1;
             if (!__all_sync(0xffffffffu, wait_bar(bar.p_full(x), (PAIR ? j : j >> 1) & 1, ctl))) goto done;
+            if (PAIR && D == 64 && jn < n_tiles) {  // P has left S's columns: the next S goes first
+                if (i == 0 && !__all_sync(0xffffffffu, wait_bar(bar.k_full(jn % C::NSK), (jn / C::NSK) & 1, ctl))) goto done;
+                tc_fence_after();
+                s_into(x, jn, i == 1);
+            }
             if (i == 0 && !__all_sync(0xffffffffu, wait_bar(bar.v_full(sv), (j / C::NSV) & 1, ctl))) goto done;
             tc_fence_after();
-            issue_pv_tmem<D>(tmem + tcol_o(PAIR ? x : 0), tmem + tcol_s(x), desc_add(dv, sv * C::TILE_BYTES), j > 0);
+            issue_pv_tmem<D>(tmem + tcol_o(PAIR ? x : 0), tmem + tcol_p<D>(x), desc_add(dv, sv * C::TILE_BYTES), j > 0);
             if (!PAIR) commit_one(bar.pv_done());
+            else if (D == 64) commit_one(bar.pv_x(x));
             if (!PAIR || i == 1) {
                 commit_one(bar.v_free(sv));
                 if (j == n_tiles - 1) commit_one(bar.o_final());
             }
-            if (jn < n_tiles) {
+            if (jn < n_tiles && !(PAIR && D == 64)) {
                 if (i == 0 && !__all_sync(0xffffffffu, wait_bar(bar.k_full(jn % C::NSK), (jn / C::NSK) & 1, ctl))) goto done;
                 tc_fence_after();
                 s_into(x, jn, !PAIR || i == 1);
@@ -843,17 +859,17 @@ __device__ __forceinline__ void hide_columns(int nv, uint32_t (&r)[32])
 // 0): O, the row sum and the probabilities of the tile's chunks before, whose second rounding
 // to bf16 is 2^-8 of that little.
 template <int D>
-__device__ __noinline__ void outgrown(uint32_t t_s, uint32_t t_o, int chunks, bool has_o, float alpha)
+__device__ __noinline__ void outgrown(uint32_t t_p, uint32_t t_o, int chunks, bool has_o, float alpha)
 {
     uint32_t r[16];
     tmem_wait_st();  // the probabilities just stored are read again
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
-        tmem_ld16_wait(t_s + c * 16, r);
+        tmem_ld16_wait(t_p + c * 16, r);
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             r[i] = pack_bf16x2(__uint_as_float(r[i] << 16) * alpha, __uint_as_float(r[i] & 0xffff0000u) * alpha);
-        tmem_st16(t_s + c * 16, r);
+        tmem_st16(t_p + c * 16, r);
     }
     if (!has_o) return;
 #pragma unroll 1
@@ -870,11 +886,13 @@ __device__ __noinline__ void outgrown(uint32_t t_s, uint32_t t_o, int chunks, bo
 // P = exp2(S * scale * log2e - m) as bf16 over the columns that S has been read from.  The first
 // tile takes its row maximum before; later a row keeps m until a chunk's probabilities sum to
 // more than 2^GROWTH (one above it, or enough of them).  m is -inf, and the row's
-// probabilities are 0, until the row has seen a key.  P V of the key tile before is complete: S of
-// this one came after it, or (one-tile units) pv_done says so.
+// probabilities are 0, until the row has seen a key.  P V of the key tile before has to be
+// complete before O is rescaled (one-tile units: pv_done), and with P in columns of its own before
+// the first of P is stored (pv_first); otherwise S of this tile came after it.
 template <int D, bool MASK>
-__device__ __forceinline__ bool chunk_softmax_tile(uint32_t t_s, uint32_t t_o, int nv, float sl2, float &m_used, float &l,
-                                                   int j, uint32_t pv_done, const Ctl &ctl)
+__device__ __forceinline__ bool chunk_softmax_tile(uint32_t t_s, uint32_t t_p, uint32_t t_o, int nv, float sl2,
+                                                   float &m_used, float &l, int j, uint32_t pv_done, uint32_t pv_first,
+                                                   const Ctl &ctl)
 {
     uint32_t ra[32], rb[32];  // the load of chunk c + 1 is in flight while chunk c is used
     if (j == 0) {
@@ -899,6 +917,10 @@ __device__ __forceinline__ bool chunk_softmax_tile(uint32_t t_s, uint32_t t_o, i
         Acc8 acc;
         exp_chunk(cur, sl2, neg_m, pk, acc);
         float lt = sum8(acc);
+        if (D == 64 && c == 0 && pv_first) {
+            ok = __all_sync(0xffffffffu, wait_bar(pv_first, (j - 1) & 1, ctl));
+            tc_fence_after();
+        }
         const bool grow = lt > limit || (MASK && m_used == -INFINITY && c * 32 < nv);
         if (__any_sync(0xffffffffu, grow)) {
             const float m_new = grow ? fmaxf(m_used, max32(cur) * sl2) : m_used;
@@ -908,7 +930,7 @@ __device__ __forceinline__ bool chunk_softmax_tile(uint32_t t_s, uint32_t t_o, i
                 tc_fence_after();
             }
             if (more) tmem_wait_ld_regs(nxt);
-            outgrown<D>(t_s, t_o, c, j > 0, alpha);
+            outgrown<D>(t_p, t_o, c, j > 0, alpha);
             l *= alpha;
             m_used = m_new;
             neg_m = m_used == -INFINITY ? 0.f : -m_used;
@@ -917,7 +939,7 @@ __device__ __forceinline__ bool chunk_softmax_tile(uint32_t t_s, uint32_t t_o, i
             lt = sum8(again);
         }
         l += lt;
-        tmem_st16(t_s + c * 16, pk);
+        tmem_st16(t_p + c * 16, pk);
     };
     tmem_ld32(t_s, ra);
 #pragma unroll 1
@@ -979,10 +1001,13 @@ __device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *s
             break;
         }
         tc_fence_after();
+        const uint32_t t_p = lane_base + tcol_p<D>(xb);
         const uint32_t pvw = one_tile ? bar.pv_done() : 0u;
+        const uint32_t pvf = D == 64 && !one_tile && j > 0 ? bar.pv_x(x) : 0u;
         const bool whole = lim_warp >= (j + 1) * BN;
-        const bool ok = whole ? chunk_softmax_tile<D, false>(t_s, t_o, BN, a.scale_log2, m_used, l, j, pvw, ctl)
-                              : chunk_softmax_tile<D, true>(t_s, t_o, lim - j * BN, a.scale_log2, m_used, l, j, pvw, ctl);
+        const bool ok = whole ? chunk_softmax_tile<D, false>(t_s, t_p, t_o, BN, a.scale_log2, m_used, l, j, pvw, pvf, ctl)
+                              : chunk_softmax_tile<D, true>(t_s, t_p, t_o, lim - j * BN, a.scale_log2, m_used, l, j, pvw,
+                                                            pvf, ctl);
         if (!ok) {
             alive = false;
             break;
