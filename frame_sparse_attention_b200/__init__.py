@@ -26,7 +26,7 @@ Python face of libsfa.so (C ABI in include/sfa.h):
 
 Tensors are PyTorch CUDA tensors; calls run on the current CUDA stream.
 """
-from ._lib import (SET_KINDS, SFA_DEBUG_STALL_GDN_STATE, SFA_DEBUG_STALL_SOFTMAX, SFA_ERR_BAD_SET, SFA_ERR_CUDA,
+from ._lib import (SET_KINDS, SFA_DEBUG_CACHE_ROWS, SFA_DEBUG_CACHE_TILES, SFA_DEBUG_STALL_GDN_STATE, SFA_DEBUG_STALL_SOFTMAX, SFA_ERR_BAD_SET, SFA_ERR_CUDA,
                    SFA_ERR_INVALID_ARG, SFA_ERR_TIMEOUT, SFA_ERR_UNSUPPORTED, SFA_OK, AttnDesc,
                    SetParams, SfaError, attn_desc, build_sets, error_string, forward, forward_blocks, forward_dual,
                    forward_host, host_workspace_bytes,
@@ -39,7 +39,7 @@ from ._cache import (CACHE_BLOCK, FrameCache, RopeTable, cache_append, cache_cre
 
 __all__ = ["CACHE_BLOCK", "FrameCache", "RopeTable", "cache_append", "cache_create", "cache_read", "cache_write",
            "forward_cache", "forward_cache_workspace_bytes", "qk_norm_rope", "rope_table",
-           "SET_KINDS", "SFA_DEBUG_STALL_GDN_STATE", "SFA_DEBUG_STALL_SOFTMAX", "SFA_ERR_BAD_SET", "SFA_ERR_CUDA",
+           "SET_KINDS", "SFA_DEBUG_CACHE_ROWS", "SFA_DEBUG_CACHE_TILES", "SFA_DEBUG_STALL_GDN_STATE", "SFA_DEBUG_STALL_SOFTMAX", "SFA_ERR_BAD_SET", "SFA_ERR_CUDA",
            "SFA_ERR_INVALID_ARG", "SFA_ERR_TIMEOUT", "SFA_ERR_UNSUPPORTED", "SFA_OK", "AttnDesc",
            "SetParams", "SfaError", "attn_desc", "build_sets", "error_string", "forward", "forward_blocks",
            "forward_dual", "forward_host", "host_workspace_bytes",

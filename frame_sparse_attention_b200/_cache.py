@@ -350,7 +350,8 @@ def forward_cache(q, cache: FrameCache, table, kv_lens, causal: bool = False, q_
     kv_lens, for the split of the work (0: all that the table can hold).  workspace: a uint8
     tensor of forward_cache_workspace_bytes (allocated here when not given).  H_kv: key heads,
     where neither the pool, the table nor kv_lens says so.  Rows that see no key give O = 0,
-    LSE = -inf, so the result merges with other branches by lse_merge."""
+    LSE = -inf, so the result merges with other branches by lse_merge.  debug_flags: SFA_DEBUG_*
+    test hooks, 0 in normal use."""
     dev = q.get_device()
     shape = _shape4("q", q)
     sq, qp = _rows("q", q, dev, shape)

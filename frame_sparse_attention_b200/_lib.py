@@ -28,6 +28,8 @@ SET_KINDS = {"dense": 0, "lvsa": 1, "local": 2, "anchor": 3, "memory": 4, "expli
 SFA_MAX_HEADS = 1024
 SFA_DEBUG_STALL_SOFTMAX = 1
 SFA_DEBUG_STALL_GDN_STATE = 2
+SFA_DEBUG_CACHE_ROWS = 4
+SFA_DEBUG_CACHE_TILES = 8
 
 
 class SfaError(RuntimeError):

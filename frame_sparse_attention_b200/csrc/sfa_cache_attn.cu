@@ -1241,18 +1241,33 @@ struct Plan {
     int64_t ctas;
 };
 
-constexpr int TILE_MIN_ROWS = 17;
+constexpr int FEW_ROWS = 32;
+
+// Which kernel.  Up to 32 query rows of a key head, 16 rows a CTA read the cache at most twice
+// and win (12 heads x 4 sequences over 8192 tokens, d = 128: 24 rows 56 against 61 us, 32 rows 57
+// against 62, 48 rows 71 against 62; 8 x 8 over 16384, d = 64: 32 rows 77 against 106, 48 rows
+// 107 against 106), and beyond that while all its steps hardly fill the SMs once, where the tile
+// kernel's start and end are most of its time (12 heads over 1560 tokens: 48 rows 13.8 against
+// 16.9, 64 rows 16.4 against 17.0, 96 rows 19.5 against 17.3; 4 heads over 300 tokens, d = 64:
+// 128 rows 7.3 against 11.5).
+bool few_rows(const sfa_cache_attn_desc *d, int64_t rows, int64_t kv)
+{
+    if (d->debug_flags & SFA_DEBUG_CACHE_TILES) return false;
+    if (d->debug_flags & SFA_DEBUG_CACHE_ROWS) return true;
+    const int64_t units = (int64_t)d->B * d->H_kv * ((rows + FR_ROWS - 1) / FR_ROWS);
+    return rows <= FEW_ROWS || 2 * units * ((kv + FR_KEYS - 1) / FR_KEYS) <= 3 * (int64_t)attn_sms() * FR_CTAS;
+}
 
 Plan plan_of(const sfa_cache_attn_desc *d, const sfa_cache *c)
 {
     Plan p;
     const int64_t rows = (int64_t)d->Lq * (d->H / d->H_kv);
-    p.tiles = rows >= TILE_MIN_ROWS;
+    int64_t kv = (int64_t)c->table_len * c->page_len;
+    if (d->max_kv > 0 && d->max_kv < kv) kv = d->max_kv;
+    p.tiles = !few_rows(d, rows, kv);
     const int tile_rows = p.tiles ? CT_ROWS : FR_ROWS, step_keys = p.tiles ? BN : FR_KEYS;
     p.row_tiles = (int)((rows + tile_rows - 1) / tile_rows);
     const int64_t units = (int64_t)d->B * d->H_kv * p.row_tiles;
-    int64_t kv = (int64_t)c->table_len * c->page_len;
-    if (d->max_kv > 0 && d->max_kv < kv) kv = d->max_kv;
     const int64_t steps = std::max<int64_t>(1, (kv + step_keys - 1) / step_keys);
     // The number of ranges per unit, by the steps that the launch takes: a range takes its own
     // steps and a fixed start and end, and the join of k ranges a little.  The lengths are on

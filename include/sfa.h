@@ -607,6 +607,11 @@ typedef struct {
     uint32_t debug_flags;      /* SFA_DEBUG_* ; 0 in normal use                            */
 } sfa_cache_attn_desc;
 
+/* Test hooks: sfa_forward_cache takes the kernel of few query rows, or that of many, whatever
+ * the sizes (it chooses by the rows of a key head and the work; both give every result). */
+#define SFA_DEBUG_CACHE_ROWS 4u
+#define SFA_DEBUG_CACHE_TILES 8u
+
 sfa_status sfa_forward_cache_workspace(const sfa_cache_attn_desc *desc, const sfa_cache *cache, size_t *bytes);
 
 sfa_status sfa_forward_cache(const sfa_cache_attn_desc *desc, const sfa_cache *cache, const void *q,

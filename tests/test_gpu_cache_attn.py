@@ -50,7 +50,7 @@ def poisoned(m, cache, table, lens, per_head):
 
 
 def run_case(B, H, Hk, L, d, P, kv, per_head=False, causal=False, ragged=False, q_ragged=False, mem="bhld", seed=0,
-             scale=None, max_kv=None, q_gain=1.0):
+             scale=None, max_kv=None, q_gain=1.0, flags=0):
     m, g = sfa(), np.random.default_rng(seed + 7 * L + kv + d)
     heads, rows = (1, Hk) if per_head else (Hk, 1)
     n = max(1, -(-kv // P))
@@ -76,7 +76,7 @@ def run_case(B, H, Hk, L, d, P, kv, per_head=False, causal=False, ragged=False, 
     out = strided(torch.full_like(q, 5.0).cuda(), mem)
     lse = torch.full((B, H, L), 5.0, device="cuda")
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    args = dict(causal=causal, scale=scale, max_kv=kv if max_kv is None else max_kv, H_kv=Hk,
+    args = dict(causal=causal, scale=scale, max_kv=kv if max_kv is None else max_kv, H_kv=Hk, debug_flags=flags,
                 q_lens=None if q_lens is None else torch.from_numpy(q_lens).cuda())
     t, ln = torch.from_numpy(table).cuda(), torch.from_numpy(lens if per_head else lens[:, 0].copy()).cuda()
     o, l = m.forward_cache(qc, cache, t, ln, out=out, lse=lse, dev_status=status, **args)
@@ -111,9 +111,13 @@ SMALL = [
 ]
 
 
+ROWS, TILES = 4, 8  # SFA_DEBUG_CACHE_*: the kernel of few rows, the kernel of many
+
+
+@pytest.mark.parametrize("flags", [0, TILES])
 @pytest.mark.parametrize("case", SMALL, ids=lambda c: "B{B}H{H}.{Hk}L{L}d{d}P{P}kv{kv}".format(**c))
-def test_few_rows(case):
-    run_case(**case)
+def test_few_rows(case, flags):
+    run_case(**case, flags=flags)
 
 
 CHUNKS = [
@@ -130,19 +134,21 @@ CHUNKS = [
 ]
 
 
+@pytest.mark.parametrize("flags", [0, ROWS, TILES])
 @pytest.mark.parametrize("case", CHUNKS, ids=lambda c: "B{B}H{H}.{Hk}L{L}d{d}P{P}kv{kv}".format(**c))
-def test_chunks(case):
-    run_case(**case)
+def test_chunks(case, flags):
+    run_case(**case, flags=flags)
 
 
+@pytest.mark.parametrize("flags", [ROWS, TILES])
 @pytest.mark.parametrize("L", [1, 140])
-def test_repeated_calls_and_the_bound_of_lengths(L):
+def test_repeated_calls_and_the_bound_of_lengths(L, flags):
     """The result does not depend on what the workspace held, and max_kv is a matter of speed."""
-    m, q, cache, t, ln, o, l, args = run_case(B=2, H=2, Hk=2, L=L, d=128, P=32, kv=1500, ragged=True)
+    m, q, cache, t, ln, o, l, args = run_case(B=2, H=2, Hk=2, L=L, d=128, P=32, kv=1500, ragged=True, flags=flags)
     args.pop("max_kv")
     for max_kv in (0, 100, 1500, 48000):
-        need = m.forward_cache_workspace_bytes(q, cache, t, ln, max_kv=max_kv)
-        ws = torch.full((max(need, 1),), 0xff, dtype=torch.uint8, device="cuda")
+        need = 64 * 4 * q.numel() // 128 * 129  # as much as 64 ranges take
+        ws = torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")
         o1, l1 = m.forward_cache(q, cache, t, ln, workspace=ws, max_kv=max_kv, **args)
         o2, l2 = m.forward_cache(q, cache, t, ln, max_kv=max_kv, **args)
         torch.cuda.synchronize()
@@ -150,16 +156,42 @@ def test_repeated_calls_and_the_bound_of_lengths(L):
         assert torch.allclose(o1.float(), o.float(), atol=2e-2, rtol=2 * U) and torch.allclose(l1, l, atol=1e-4)
 
 
+@pytest.mark.parametrize("flags", [ROWS, TILES])
 @pytest.mark.parametrize("L", [3, 200])
 @pytest.mark.parametrize("gain", [30.0, 1e-3])
-def test_sharp_and_flat_scores(L, gain):
+def test_sharp_and_flat_scores(L, gain, flags):
     # growing maxima (a late key that beats the earlier ones by far) and equal scores
-    run_case(B=1, H=2, Hk=1, L=L, d=128, P=64, kv=700, q_gain=gain)
-    run_case(B=1, H=2, Hk=1, L=L, d=64, P=64, kv=700, q_gain=gain, causal=True)
+    run_case(B=1, H=2, Hk=1, L=L, d=128, P=64, kv=700, q_gain=gain, flags=flags)
+    run_case(B=1, H=2, Hk=1, L=L, d=64, P=64, kv=700, q_gain=gain, causal=True, flags=flags)
 
 
+@pytest.mark.parametrize("flags", [ROWS, TILES])
+@pytest.mark.parametrize("L", [3, 100, 200])
+def test_scores_that_grow_from_key_to_key(L, flags):
+    """Every key beats the ones before by more than the running maximum may lag: each chunk of
+    every tile rescales what came before."""
+    m, d, n = sfa(), 64, 300
+    cache = empty_pool(m, 19, 1, 16, d)
+    k = torch.zeros(1, 1, n, d)
+    k[..., 0] = torch.arange(n).float() * 0.5  # scores 0.125 * 64 * 0.5 j = 4 j: a factor e^4 from key to key
+    v = torch.randn(1, 1, n, d, generator=torch.Generator().manual_seed(1))
+    table = torch.arange(19, dtype=torch.int32, device="cuda").reshape(1, 19)
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    m.cache_write(cache, k.bfloat16().cuda(), v.bfloat16().cuda(), table, zero)
+    q = torch.zeros(1, 1, L, d)
+    q[..., 0] = 64.0
+    q[..., 1:] = torch.randn(L, d - 1, generator=torch.Generator().manual_seed(2))
+    q = q.bfloat16().cuda()
+    kk, vv = gather(cache, table.unsqueeze(1).cpu().numpy(), 0, 0, n)
+    for causal in (False, True):
+        o, l = m.forward_cache(q, cache, table, zero + n, causal=causal, debug_flags=flags)
+        torch.cuda.synchronize()
+        check(o[0, 0], l[0, 0], f64(q[0, 0]), kk, vv, 0.125, causal)
+
+
+@pytest.mark.parametrize("flags", [ROWS, TILES])
 @pytest.mark.parametrize("L", [2, 150])
-def test_large_scales_take_the_second_product(L):
+def test_large_scales_take_the_second_product(L, flags):
     """Blocks with exponents above 7 (magnitudes of 57344 and more), next to ordinary ones."""
     m, g = sfa(), np.random.default_rng(3)
     d, n = 128, 200
@@ -169,15 +201,17 @@ def test_large_scales_take_the_second_product(L):
         b[1:3, :, ::3, 1] = to
     table = np.array([[[2, 0, 1, 3]]], np.int32)
     q = torch.from_numpy(1e-5 * g.standard_normal((1, 1, L, d))).bfloat16()
-    o, l = m.forward_cache(q.cuda(), cache, torch.from_numpy(table).cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"))
+    o, l = m.forward_cache(q.cuda(), cache, torch.from_numpy(table).cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"),
+                           debug_flags=flags)
     torch.cuda.synchronize()
     k, v = gather(cache, table, 0, 0, n)
     check(o[0, 0], l[0, 0], f64(q[0, 0]), k, v, 1 / math.sqrt(d), False)
 
 
+@pytest.mark.parametrize("flags", [ROWS, TILES])
 @pytest.mark.parametrize("L", [1, 130])
 @pytest.mark.parametrize("what", ["length", "negative length", "page"])
-def test_bad_lengths_and_pages_are_reported(L, what):
+def test_bad_lengths_and_pages_are_reported(L, what, flags):
     m, g = sfa(), np.random.default_rng(4)
     cache = random_pool(g, m, 6, 1, 16, 64)
     table = np.array([[[0, 1, 2]], [[3, 4, 5]]], np.int32)
@@ -190,7 +224,8 @@ def test_bad_lengths_and_pages_are_reported(L, what):
     else:
         table[1, 0, 1] = 6
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    o, l = m.forward_cache(q, cache, torch.from_numpy(table).cuda(), torch.from_numpy(lens).cuda(), dev_status=status)
+    o, l = m.forward_cache(q, cache, torch.from_numpy(table).cuda(), torch.from_numpy(lens).cuda(), dev_status=status,
+                           debug_flags=flags)
     torch.cuda.synchronize()
     assert status.item() == m.SFA_ERR_BAD_SET
     k, v = gather(cache, table, 0, 0, 40)  # the other sequence is right
@@ -199,7 +234,7 @@ def test_bad_lengths_and_pages_are_reported(L, what):
 
 @pytest.mark.parametrize("L", [1, 129])
 def test_other_stream_and_graph_replay(L):
-    m, q, cache, t, ln, o, l, args = run_case(B=1, H=2, Hk=2, L=L, d=64, P=32, kv=900)
+    m, q, cache, t, ln, o, l, args = run_case(B=1, H=2, Hk=2, L=L, d=64, P=32, kv=900, flags=TILES if L > 1 else ROWS)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
@@ -277,9 +312,9 @@ def test_offsets_past_32_bits():
     m.cache_write(cache, x, x, table, zero)
     n = torch.tensor([300], dtype=torch.int32, device="cuda")
     back = C.dequantise(*C.quantise(f64(x[0, 0])))
-    for L in (1, 150):
+    for L, flags in ((1, ROWS), (150, TILES)):
         q = torch.randn(1, 1, L, d, device="cuda").bfloat16()
-        o, l = m.forward_cache(q, cache, table, n)
+        o, l = m.forward_cache(q, cache, table, n, debug_flags=flags)
         torch.cuda.synchronize()
         check(o[0, 0], l[0, 0], f64(q[0, 0]), back, back, 1 / math.sqrt(d), False)
 
@@ -287,14 +322,22 @@ def test_offsets_past_32_bits():
 def test_a_wait_that_runs_out_is_reported():
     """The softmax withholds its first probabilities (a test hook): the waits run out after their
     limit, the call reports it and returns, and the next call is right."""
-    m, q, cache, t, ln, o, l, args = run_case(B=1, H=2, Hk=2, L=300, d=128, P=32, kv=700)
+    m, q, cache, t, ln, o, l, args = run_case(B=1, H=2, Hk=2, L=300, d=128, P=32, kv=700, flags=TILES)
     for n in (300, 100):  # two query tiles, one
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
-        m.forward_cache(q[:, :, :n], cache, t, ln, dev_status=status, timeout_us=2000,
-                        debug_flags=m.SFA_DEBUG_STALL_SOFTMAX, **args)
+        args["debug_flags"] = TILES | m.SFA_DEBUG_STALL_SOFTMAX
+        m.forward_cache(q[:, :, :n], cache, t, ln, dev_status=status, timeout_us=2000, **args)
         torch.cuda.synchronize()
         assert status.item() == m.SFA_ERR_TIMEOUT
         status.zero_()
+        args["debug_flags"] = TILES
         o2, l2 = m.forward_cache(q, cache, t, ln, dev_status=status, **args)
         torch.cuda.synchronize()
         assert status.item() == 0 and torch.equal(o2, o) and torch.equal(l2, l)
+
+
+def test_the_choice_of_kernel_by_size():
+    """Rows and work on both sides of the choice, without a hook."""
+    for L, B in ((31, 1), (32, 2), (33, 1), (40, 5)):
+        run_case(B=B, H=4, Hk=4, L=L, d=64, P=32, kv=1100, ragged=True)
+    run_case(B=2, H=6, Hk=6, L=130, d=128, P=64, kv=1400, per_head=True, causal=True)
