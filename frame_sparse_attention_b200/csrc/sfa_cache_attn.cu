@@ -102,6 +102,67 @@ __device__ __forceinline__ int64_t row_id(const ChunkArgs &a, const Unit &u, int
     return ((int64_t)u.b * a.H + u.hk * a.G + (r - tok * a.G)) * a.Lq + tok;
 }
 
+// Thirty-two rows of a unit, N apart from one access to the next: f(access, element offset, whether
+// the row is there) under the given strides of a query head and a token.  Row r is token r / G of
+// head r % G; the offset of a row that is not there is 0.
+struct RowWalk {
+    int r, tok, head;
+    __device__ __forceinline__ RowWalk(const ChunkArgs &a, const Unit &u, int first)
+    {
+        r = first;
+        tok = a.G == 1 ? first : first / a.G;
+        head = first - tok * a.G;
+    }
+    template <int N, typename F>
+    __device__ __forceinline__ void each(const ChunkArgs &a, const Unit &u, int64_t head_stride, int64_t tok_stride,
+                                         F f) const
+    {
+        int64_t at = (u.hk * a.G + head) * head_stride + tok * tok_stride;
+        const int n = u.n_rows - r;  // rows from the first on
+        if (a.G == 1) {
+            const int64_t step = N * tok_stride;
+#pragma unroll 4
+            for (int i = 0; i < 32 / N; ++i) {
+                f(i, i * N < n ? at : 0, i * N < n);
+                at += step;
+            }
+            return;
+        }
+        const int64_t next_tok = tok_stride - a.G * head_stride;
+        int h = head;
+#pragma unroll 4
+        for (int i = 0; i < 32 / N; ++i) {
+            f(i, i * N < n ? at : 0, i * N < n);
+            at += N * head_stride;
+            h += N;
+            while (h >= a.G) {
+                h -= a.G;
+                at += next_tok;
+            }
+        }
+    }
+};
+
+// Stores 16-byte pieces four at a time, so that as many reads of shared memory are under way.
+template <typename T>
+struct RowOut {
+    T *dst;
+    uint4 v[4];
+    int64_t at[4];
+    bool on[4];
+    __device__ __forceinline__ explicit RowOut(T *d) : dst(d) {}
+    __device__ __forceinline__ void put(int i, const uint4 &x, int64_t offset, bool there)
+    {
+        v[i & 3] = x;
+        at[i & 3] = offset;
+        on[i & 3] = there;
+        if ((i & 3) != 3) return;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (on[k]) *reinterpret_cast<uint4 *>(dst + at[k]) = v[k];
+    }
+};
+
 // A CTA without a range of its own leaves "nothing seen" for its rows.
 __device__ __forceinline__ void skip_range(const ChunkArgs &a, const Unit &u, int tile_rows)
 {
@@ -970,13 +1031,12 @@ __device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *s
     static_assert(C::SMEM_V >= 4 * C::TILE_BYTES, "two tiles of fp32 rows end before the V slots");
     // This warp's 32 query rows, whole rows at a time, all under way at once.  (What a CTA does
     // once is kept in short loops: unrolled, it ran at the rate that its instructions came in.)
-#pragma unroll 1
-    for (int i = lane / LR; i < 32; i += RPI) {
-        const int rr = warp * 32 + i, r = tile_row0 + rr;
-        const int tok = a.G == 1 ? r : r / a.G, head = a.G == 1 ? 0 : r - tok * a.G;
-        const bool there = r < u.n_rows;
-        const uint16_t *src = a.q + u.b * a.qs[0] + (u.hk * a.G + head) * a.qs[1] + tok * a.qs[2] + (lane % LR) * 8;
-        cp_async16(s_tile + swz<D>(rr, lane % LR), there ? src : a.q, there);
+    {
+        const RowWalk w(a, u, tile_row0 + warp * 32 + lane / LR);
+        const uint16_t *q = a.q + u.b * a.qs[0] + (lane % LR) * 8;
+        w.each<RPI>(a, u, a.qs[1], a.qs[2], [&](int i, int64_t at, bool there) {
+            cp_async16(s_tile + swz<D>(warp * 32 + i * RPI + lane / LR, lane % LR), q + at, there);
+        });
     }
     cp_async_wait_all();
     fence_proxy_async_smem();  // before the block meets: Q is there for the tensor cores after it
@@ -1065,23 +1125,21 @@ __device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *s
     __syncwarp();  // a warp stores the 32 rows that its lanes have staged, whole rows at a time
     if (a.n_split > 1) {
         constexpr int PL = D / 4, PR = 32 / PL;  // lanes per fp32 row, rows per access
-#pragma unroll 2
-        for (int i = 0; i < 32; i += PR) {
-            const int rr = warp * 32 + i + lane / PL, ch = lane % PL, ro = tile_row0 + rr;
-            if (ro < u.n_rows)
-                *reinterpret_cast<uint4 *>(a.part_o + (u.split * part_rows + row_id(a, u, ro)) * D + ch * 4) =
-                    *reinterpret_cast<const uint4 *>(smem + (s_part - sbase) + rr * D * 4 + ((ch ^ (rr & 7)) << 4));
-        }
+        const RowWalk w(a, u, tile_row0 + warp * 32 + lane / PL);
+        float *dst = a.part_o + (u.split * part_rows + (int64_t)u.b * a.H * a.Lq) * D + (lane % PL) * 4;
+        RowOut<float> rows(dst);
+        w.each<PR>(a, u, (int64_t)a.Lq * D, D, [&](int i, int64_t at, bool on) {
+            const int rr = warp * 32 + i * PR + lane / PL;
+            rows.put(i, lds16(s_part + rr * D * 4 + (((lane % PL) ^ (rr & 7)) << 4)), at, on);
+        });
         return;
     }
-#pragma unroll 2
-    for (int i = 0; i < 32; i += RPI) {
-        const int rr = warp * 32 + i + lane / LR, ch = lane % LR, ro = tile_row0 + rr;
-        const int tok = a.G == 1 ? ro : ro / a.G, head = a.G == 1 ? 0 : ro - tok * a.G;
-        if (ro < u.n_rows)
-            *reinterpret_cast<uint4 *>(a.o + u.b * a.os[0] + (u.hk * a.G + head) * a.os[1] + tok * a.os[2] + ch * 8) =
-                *reinterpret_cast<const uint4 *>(smem + (s_tile - sbase) + swz<D>(rr, ch));
-    }
+    const RowWalk w(a, u, tile_row0 + warp * 32 + lane / LR);
+    uint16_t *dst = a.o + u.b * a.os[0] + (lane % LR) * 8;
+    RowOut<uint16_t> rows(dst);
+    w.each<RPI>(a, u, a.os[1], a.os[2], [&](int i, int64_t at, bool on) {
+        rows.put(i, lds16(s_tile + swz<D>(warp * 32 + i * RPI + lane / LR, lane % LR)), at, on);
+    });
 }
 
 template <int D>
