@@ -27,9 +27,14 @@
 namespace sfa {
 namespace {
 
-constexpr int ROW_WARPS = 8;  // warps per CTA
-constexpr int ROW_CTAS = 4;   // CTAs per SM: 64 registers a thread, 32 warps (24 warps with 80: 154 against 143 us
+constexpr int ROW_WARPS = 4;  // warps per CTA (8: a token's append 4.3 against 4.1 us, 9000 tokens' 34.1 against 33.8)
+constexpr int ROW_CTAS = 8;   // CTAs per SM: 64 registers a thread, 32 warps (24 warps with 80: 154 against 143 us
                               // on 63960 tokens of 12 + 12 heads, and 33 against 29 on the append of 4680)
+// Rows of a lane under way together where a warp takes consecutive rows, D / 8 lanes to a row.
+// Written, 12 heads, d = 128, 1560, 4680 and 20280 tokens: two 4.1, 11.1, 33.6 us, four 4.3, 12.0, 32.9.
+constexpr int WRITE_U = 2, READ_U = 4;
+template <int D>
+constexpr int ROWS_AT_ONCE = 32 * 8 / D;
 
 struct RowsArgs {
     int32_t B, H, Hk, L;
@@ -53,6 +58,7 @@ struct RowsArgs {
     int32_t *status;
     int32_t n_parts;   // warps per token
     uint32_t n_warps;  // B * L * n_parts
+    uint32_t rows;     // B * Hk * L
 };
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -119,11 +125,6 @@ template <int D, bool HALF>
 __device__ __forceinline__ void coefficients(Coef &f, const float *cosp, const float *sinp, const float *w, int e0, int R)
 {
     float A[8], B[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        A[j] = 1.f;
-        B[j] = 0.f;
-    }
     const bool first = HALF && e0 < R / 2;
     const int mate0 = !HALF ? e0 : first ? e0 + R / 2 : e0 < R ? e0 - R / 2 : e0;  // where the mates' weights lie
     float wo[8], wm[8];
@@ -139,15 +140,28 @@ __device__ __forceinline__ void coefficients(Coef &f, const float *cosp, const f
 #pragma unroll
         for (int j = 0; j < 8; ++j) wo[j] = wm[j] = 1.f;
     }
+    // the lane's pairs: four (interleaved), or eight from the first half's on; past the rotated
+    // part the tables hold cosine 1 and sine 0
+    float c[8], t[8];
+#pragma unroll
+    for (int j = 0; j < (HALF ? 8 : 4); j += 4) {
+        const int p = HALF ? (first || e0 >= R ? e0 % (D / 2) : mate0) + j : e0 / 2;
+        const float4 x = *reinterpret_cast<const float4 *>(cosp + p), y = *reinterpret_cast<const float4 *>(sinp + p);
+        c[j] = x.x, c[j + 1] = x.y, c[j + 2] = x.z, c[j + 3] = x.w;
+        t[j] = y.x, t[j + 1] = y.y, t[j + 2] = y.z, t[j + 3] = y.w;
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        A[j] = wo[j];
-        if (e0 + j < R) {
-            const int p = HALF ? (first ? e0 : mate0) + j : (e0 + j) >> 1;
-            const float c = cosp[p], s = sinp[p];
-            A[j] = wo[j] * c;
-            const bool minus = HALF ? first : (j & 1) == 0;
-            B[j] = (HALF ? wm[j] : wo[j ^ 1]) * (minus ? -s : s);
+        const int p = HALF ? j : j >> 1;
+        const bool minus = HALF ? first : (j & 1) == 0;
+        A[j] = wo[j] * c[p];
+        B[j] = (HALF ? wm[j] : wo[j ^ 1]) * (minus ? -t[p] : t[p]);
+    }
+    if (R < D) {  // elements that do not turn, whatever their neighbours' weights
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            A[j] = e0 + j < R ? A[j] : wo[j];
+            B[j] = e0 + j < R ? B[j] : 0.f;
         }
     }
 #pragma unroll
@@ -245,7 +259,7 @@ __device__ __forceinline__ uint32_t make_finite(uint32_t w)
 // Store this lane's eight elements of a row as codes (and, one lane per block, the scale).
 // row < 0: nothing is stored.  Every lane of the warp calls it.
 template <int D>
-__device__ __forceinline__ void store_row(uint8_t *codes, uint8_t *scales, int64_t row, uint4 raw, int e0,
+__device__ __forceinline__ void store_row(uint8_t *codes, uint8_t *scales, int row, uint4 raw, int e0,
                                           int32_t *status)
 {
     uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -256,36 +270,58 @@ __device__ __forceinline__ void store_row(uint8_t *codes, uint8_t *scales, int64
         for (int j = 0; j < 4; ++j) w[j] = make_finite(w[j]);
         top = block_amax(w);
     }
-    const int e = block_exponent(top);
-    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e; the products are exact
+    const uint32_t t = block_exponent_bits(top);
+    const float inv = __uint_as_float(((127u + 8u + 127u) << 23) - (t << 16));  // 2^-e; the products are exact
     const uint64_t inv2 = f2(inv, inv);
     const Eight x = unpack8(w);
-    uint32_t c4[4];
+    uint32_t c4[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const uint64_t ye = mul2(x.e[i], inv2), yo = mul2(x.o[i], inv2);
-        c4[2 * i] = to_e4m3x2(lo2(ye), lo2(yo));
-        c4[2 * i + 1] = to_e4m3x2(hi2(ye), hi2(yo));
+        c4[i] = to_e4m3x4(lo2(ye), lo2(yo), hi2(ye), hi2(yo));
     }
-    const uint2 c = make_uint2(c4[0] | (c4[1] << 16), c4[2] | (c4[3] << 16));
+    const uint2 c = make_uint2(c4[0], c4[1]);
     if (row >= 0) {
-        *reinterpret_cast<uint2 *>(codes + row * D + e0) = c;
-        if ((e0 & (CACHE_BLOCK - 1)) == 0) scales[row * (D / CACHE_BLOCK) + e0 / CACHE_BLOCK] = (uint8_t)(e + 127);
+        *reinterpret_cast<uint2 *>(codes + (int64_t)row * D + e0) = c;
+        if ((e0 & (CACHE_BLOCK - 1)) == 0)
+            scales[(int64_t)row * (D / CACHE_BLOCK) + e0 / CACHE_BLOCK] = (uint8_t)((t >> 7) - 8u);
     }
 }
+
+// The rows of a token's key or value heads that a lane visits, from head `head` on in steps of
+// `hs`.  The place moves on by an addition: the kernel is bound by what it issues, half of that
+// integer instructions, and a 64-bit product per row made 20280 tokens' append 73.9, not 72.4 us.
+struct HeadRows {
+    const uint16_t *p;
+    int64_t inc;
+    int head, hs, n;
+    __device__ __forceinline__ HeadRows(const uint16_t *base, int b, int h, int i, int e0, int step,
+                                        const int64_t (&s)[3], int heads)
+        : p(base + (b * s[0] + h * s[1] + i * s[2] + e0)), inc(step * s[1]), head(h), hs(step), n(heads)
+    {
+    }
+    __device__ __forceinline__ uint4 load()
+    {
+        const uint4 r = head < n ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0u, 0u, 0u, 0u);
+        p += inc;
+        head += hs;
+        return r;
+    }
+};
 
 // One warp per token, or one of n_parts warps that share a token's row groups: groups
 // [0, Gq) are the query heads, [Gq, Gq + Gk) the key (and value) heads, RW heads a group,
 // and part p takes the groups g = p mod n_parts.  The loads of the first U groups go out
 // before the angles are formed, and a group's registers are loaded again as soon as it is
-// done, so a warp has U (CACHE: a pair of) rows under way throughout.
+// done, so a warp has rows under way throughout.  With the cache, a lane looks up the place of
+// one of the part's key rows before any is stored.
 template <int D, bool HALF, bool CACHE>
 __global__ void __launch_bounds__(ROW_WARPS * 32, ROW_CTAS) rows_kernel(const __grid_constant__ RowsArgs a)
 {
     constexpr int G = D / 8;     // lanes per row
     constexpr int RW = 32 / G;   // rows of a group
     constexpr int U = CACHE ? 2 : 4;  // groups under way (append, U = 4: 31 against 29 us)
-    __shared__ float cos_all[ROW_WARPS][D / 2], sin_all[ROW_WARPS][D / 2];
+    __shared__ __align__(16) float cos_all[ROW_WARPS][D / 2], sin_all[ROW_WARPS][D / 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t w = blockIdx.x * (uint32_t)ROW_WARPS + warp;
     if (w >= a.n_warps) return;
@@ -295,7 +331,7 @@ __global__ void __launch_bounds__(ROW_WARPS * 32, ROW_CTAS) rows_kernel(const __
     if (a.lens && i >= __ldg(a.lens + b)) return;  // a padded row (the whole warp)
     const int sub = lane / G, e0 = (lane % G) * 8;
     const int Gq = a.q ? (a.H + RW - 1) / RW : 0;
-    const int Gk = (a.k || a.v) ? (a.Hk + RW - 1) / RW : 0;
+    const int Gk = a.k ? (a.Hk + RW - 1) / RW : 0;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     const int step = a.n_parts;
 
@@ -304,23 +340,35 @@ __global__ void __launch_bounds__(ROW_WARPS * 32, ROW_CTAS) rows_kernel(const __
         const int h = g * RW + sub;
         return g < Gq && h < a.H ? *reinterpret_cast<const uint4 *>(q_src + h * a.qs[1]) : zero;
     };
-    const uint16_t *k_src = a.k + b * a.ks[0] + i * a.ks[2] + e0, *v_src = a.v + b * a.vs[0] + i * a.vs[2] + e0;
+    const uint16_t *k_src = a.k + b * a.ks[0] + i * a.ks[2] + e0;
     auto load_k = [&](int g) {
         const int h = g * RW + sub;
         return g < Gk && h < a.Hk ? *reinterpret_cast<const uint4 *>(k_src + h * a.ks[1]) : zero;
     };
-    auto load_v = [&](int g) {
-        const int h = g * RW + sub;
-        return g < Gk && h < a.Hk ? *reinterpret_cast<const uint4 *>(v_src + h * a.vs[1]) : zero;
+    // this part's first key group: g + Gq = part mod n_parts
+    const int first = (part + step - Gq % step) % step;
+    // The cache rows of G of its groups from the m0-th on, one of their rows per lane: where the
+    // sequence starts, then the row (or -1).
+    auto my_head = [&](int m0) {
+        const int g = first + (m0 + lane / RW) * step, h = g * RW + lane % RW;
+        return g < Gk && h < a.Hk ? h : -1;
+    };
+    auto my_start = [&](int h) { return h < 0 ? 0 : __ldg(a.start + b * a.ss0 + h * a.ss1); };
+    auto my_row = [&](int h, int start) {
+        if (h < 0) return -1;
+        const int row = (int)cache_row(a.cache, b, h, (int64_t)start + i);
+        if (row < 0) report_status(a.status, SFA_ERR_BAD_SET);
+        return row;
     };
     uint4 x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) x[u] = load_q(part + u * step);
+    const int start0 = CACHE ? my_start(my_head(0)) : 0;
 
     float *cosp = cos_all[warp], *sinp = sin_all[warp];
     const int32_t *pos = a.R ? a.pos + b * a.ps0 + i * a.ps1 : nullptr;
-    for (int p = lane; p < a.R / 2; p += 32) {
-        const float2 r = rotation(a, pos, p);
+    for (int p = lane; p < D / 2; p += 32) {
+        const float2 r = p < a.R / 2 ? rotation(a, pos, p) : make_float2(1.f, 0.f);
         cosp[p] = r.x;
         sinp[p] = r.y;
     }
@@ -341,10 +389,7 @@ __global__ void __launch_bounds__(ROW_WARPS * 32, ROW_CTAS) rows_kernel(const __
             }
         }
     }
-    // this part's first key group: g + Gq = part mod n_parts
-    const int first = (part + step - Gq % step) % step;
     if (first >= Gk) return;
-    const bool plain = a.eps < 0.f && a.R == 0 && !a.k_weight;  // keys stored as they are
     if (!CACHE) {
 #pragma unroll
         for (int u = 0; u < U; ++u) x[u] = load_k(first + u * step);
@@ -361,38 +406,56 @@ __global__ void __launch_bounds__(ROW_WARPS * 32, ROW_CTAS) rows_kernel(const __
             }
         }
     } else {
-        constexpr int UK = U / 2;
-        uint4 y[UK];
-        int start[UK];  // of the group's heads
-        auto load_start = [&](int g) {
-            const int h = min(g * RW + sub, a.Hk - 1);
-            return __ldg(a.start + b * a.ss0 + h * a.ss1);
-        };
-#pragma unroll
-        for (int u = 0; u < UK; ++u) {
-            x[u] = load_k(first + u * step);
-            y[u] = load_v(first + u * step);
-            start[u] = load_start(first + u * step);
-        }
-        if (!plain) coefficients<D, HALF>(f, cosp, sinp, a.k_weight, e0, a.R);
-        for (int g0 = first; g0 < Gk; g0 += UK * step) {
-#pragma unroll
-            for (int u = 0; u < UK; ++u) {
-                const int g = g0 + u * step, h = g * RW + sub;
+        coefficients<D, HALF>(f, cosp, sinp, a.k_weight, e0, a.R);
+        HeadRows k(a.k, b, first * RW + sub, i, e0, step * RW, a.ks, a.Hk);
+        HeadRows v(a.v, b, first * RW + sub, i, e0, step * RW, a.vs, a.Hk);
+        uint4 kk = k.load(), vv = v.load();
+        for (int m0 = 0; first + m0 * step < Gk; m0 += G) {
+            const int mine = my_head(m0), row = my_row(mine, m0 ? my_start(mine) : start0);
+            for (int m = m0; m < m0 + G; ++m) {
+                const int g = first + m * step;
                 if (g >= Gk) break;
-                int64_t row = -1;
-                if (h < a.Hk) {
-                    row = cache_row(a.cache, b, h, (int64_t)start[u] + i);
-                    if (row < 0) report_status(a.status, SFA_ERR_BAD_SET);
-                }
-                const uint4 kk = plain ? x[u] : norm_rotate<D, HALF>(x[u], f, a.eps, e0, a.R), vv = y[u];
-                x[u] = load_k(g + UK * step);
-                y[u] = load_v(g + UK * step);
-                start[u] = load_start(g + UK * step);
-                store_row<D>(a.cache.k, a.cache.k_scale, row, kk, e0, a.status);
-                store_row<D>(a.cache.v, a.cache.v_scale, row, vv, e0, a.status);
+                const int at = __shfl_sync(0xffffffffu, row, (m - m0) * RW + sub);
+                const uint4 y = norm_rotate<D, HALF>(kk, f, a.eps, e0, a.R), z = vv;
+                kk = k.load();
+                vv = v.load();
+                store_row<D>(a.cache.k, a.cache.k_scale, at, y, e0, a.status);
+                store_row<D>(a.cache.v, a.cache.v_scale, at, z, e0, a.status);
             }
         }
+    }
+}
+
+// Keys and values stored as they are: a warp takes consecutive rows of the (b, h, i)
+// order; a lane looks up the place of one of them while they load.
+template <int D>
+__global__ void __launch_bounds__(ROW_WARPS * 32) cache_write_kernel(const __grid_constant__ RowsArgs a)
+{
+    constexpr int G = D / 8;    // lanes per row
+    constexpr int RW = ROWS_AT_ONCE<D>;
+    constexpr int STEP = RW * WRITE_U;
+    const int lane = threadIdx.x & 31, sub = lane / G, e0 = (lane % G) * 8;
+    const uint32_t first = (blockIdx.x * ROW_WARPS + (threadIdx.x >> 5)) * STEP;
+    if (first >= a.rows) return;
+    const uint32_t r = min(first + lane % STEP, a.rows - 1), bh = r / (uint32_t)a.L;
+    const int i = (int)(r - bh * (uint32_t)a.L), b = (int)(bh / (uint32_t)a.Hk), h = (int)(bh - b * (uint32_t)a.Hk);
+    const int64_t ko = b * a.ks[0] + h * a.ks[1] + i * a.ks[2], vo = b * a.vs[0] + h * a.vs[1] + i * a.vs[2];
+    uint4 x[WRITE_U], y[WRITE_U];
+#pragma unroll
+    for (int u = 0; u < WRITE_U; ++u) {
+        x[u] = *reinterpret_cast<const uint4 *>(a.k + __shfl_sync(0xffffffffu, ko, u * RW + sub) + e0);
+        y[u] = *reinterpret_cast<const uint4 *>(a.v + __shfl_sync(0xffffffffu, vo, u * RW + sub) + e0);
+    }
+    int row = -1;
+    if (lane < STEP && first + lane < a.rows && !(a.lens && i >= __ldg(a.lens + b))) {
+        row = (int)cache_row(a.cache, b, h, (int64_t)__ldg(a.start + b * a.ss0 + h * a.ss1) + i);
+        if (row < 0) report_status(a.status, SFA_ERR_BAD_SET);
+    }
+#pragma unroll
+    for (int u = 0; u < WRITE_U; ++u) {
+        const int p = __shfl_sync(0xffffffffu, row, u * RW + sub);
+        store_row<D>(a.cache.k, a.cache.k_scale, p, x[u], e0, a.status);
+        store_row<D>(a.cache.v, a.cache.v_scale, p, y[u], e0, a.status);
     }
 }
 
@@ -426,19 +489,14 @@ __device__ __forceinline__ uint4 from_codes(uint2 c, uint32_t scale_byte)
 // looking up its own, 20280 tokens of 12 heads, d = 128, took 43.7 us, now 33.4 (5.65 TB/s), and
 // 60000 tokens 119, now 89 (6.3 TB/s).  Longer stretches a warp: 33.3 and 93 (16 CTAs per SM) to
 // 37.8 and 104 (4).
-constexpr int READ_WARPS = 8;
-constexpr int READ_U = 4;
 template <int D>
-constexpr int READ_STEP = 32 * 8 / D * READ_U;
-
-template <int D>
-__global__ void __launch_bounds__(READ_WARPS * 32) cache_read_kernel(const __grid_constant__ ReadArgs a)
+__global__ void __launch_bounds__(ROW_WARPS * 32) cache_read_kernel(const __grid_constant__ ReadArgs a)
 {
     constexpr int G = D / 8;    // lanes per row
-    constexpr int RW = 32 / G;  // rows of a warp's load
-    constexpr int STEP = READ_STEP<D>;
+    constexpr int RW = ROWS_AT_ONCE<D>;
+    constexpr int STEP = RW * READ_U;
     const int lane = threadIdx.x & 31, sub = lane / G, e0 = (lane % G) * 8;
-    const uint32_t first = (blockIdx.x * READ_WARPS + (threadIdx.x >> 5)) * STEP;
+    const uint32_t first = (blockIdx.x * ROW_WARPS + (threadIdx.x >> 5)) * STEP;
     if (first >= a.rows) return;
     const uint32_t r = min(first + lane % STEP, a.rows - 1), bh = r / (uint32_t)a.L;
     const int i = (int)(r - bh * (uint32_t)a.L), b = (int)(bh / (uint32_t)a.Hk), h = (int)(bh - b * (uint32_t)a.Hk);
@@ -539,7 +597,7 @@ template <bool CACHE>
 sfa_status launch_rows(RowsArgs &a, int d, bool half, cudaStream_t s)
 {
     const int rw = 32 / (d / 8);
-    const int groups = (a.q ? (a.H + rw - 1) / rw : 0) + ((a.k || a.v) ? (a.Hk + rw - 1) / rw : 0);
+    const int groups = (a.q ? (a.H + rw - 1) / rw : 0) + (a.k ? (a.Hk + rw - 1) / rw : 0);
     const int64_t tokens = (int64_t)a.B * a.L;
     // Warps per token: one (the angles are formed once) while the tokens alone give every SM
     // 16 warps, else as many as do, at most one per row group.  (Norm and rotation of 12 + 12
@@ -641,7 +699,14 @@ extern "C" sfa_status sfa_cache_write(const sfa_rows_desc *d, const sfa_cache *c
     a.L = d->L;
     a.eps = -1.f;
     fill_cache(a, d, cache, k, v, start, lens, dev_status);
-    return launch_rows<true>(a, d->d, false, as_cuda(stream));
+    const int64_t rows = (int64_t)d->B * d->H_kv * d->L;
+    if ((int64_t)d->B * d->L >= ((int64_t)1 << 31) || rows >= ((int64_t)1 << 31)) return SFA_ERR_INVALID_ARG;
+    a.rows = (uint32_t)rows;
+    const int per_cta = ROW_WARPS * WRITE_U * (d->d == 128 ? ROWS_AT_ONCE<128> : ROWS_AT_ONCE<64>);
+    const unsigned grid = (unsigned)((rows + per_cta - 1) / per_cta);
+    if (d->d == 128) cache_write_kernel<128><<<grid, ROW_WARPS * 32, 0, as_cuda(stream)>>>(a);
+    else cache_write_kernel<64><<<grid, ROW_WARPS * 32, 0, as_cuda(stream)>>>(a);
+    return launch_status();
 }
 
 extern "C" sfa_status sfa_cache_append(const sfa_rows_desc *d, const sfa_rope *rope, const sfa_cache *cache,
@@ -707,9 +772,9 @@ extern "C" sfa_status sfa_cache_read(const sfa_rows_desc *d, const sfa_cache *ca
     const int64_t rows = (int64_t)d->B * d->H_kv * d->L;
     if ((int64_t)d->B * d->L >= ((int64_t)1 << 31) || rows >= ((int64_t)1 << 31)) return SFA_ERR_INVALID_ARG;
     a.rows = (uint32_t)rows;
-    const int per_cta = READ_WARPS * (d->d == 128 ? READ_STEP<128> : READ_STEP<64>);
+    const int per_cta = ROW_WARPS * READ_U * (d->d == 128 ? ROWS_AT_ONCE<128> : ROWS_AT_ONCE<64>);
     const unsigned grid = (unsigned)((rows + per_cta - 1) / per_cta);
-    if (d->d == 128) cache_read_kernel<128><<<grid, READ_WARPS * 32, 0, as_cuda(stream)>>>(a);
-    else cache_read_kernel<64><<<grid, READ_WARPS * 32, 0, as_cuda(stream)>>>(a);
+    if (d->d == 128) cache_read_kernel<128><<<grid, ROW_WARPS * 32, 0, as_cuda(stream)>>>(a);
+    else cache_read_kernel<64><<<grid, ROW_WARPS * 32, 0, as_cuda(stream)>>>(a);
     return launch_status();
 }

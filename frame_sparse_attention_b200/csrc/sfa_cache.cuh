@@ -105,17 +105,25 @@ struct CachePlace {
 // e of a block whose largest magnitude has the bf16 bits `amax` (finite, sign cleared): the
 // smallest e with amax <= 448 * 2^e = 1.75 * 2^(e + 8).  For amax = (1 + m / 128) * 2^E that
 // is E - 8, one more where m > 96; adding 31 carries into the exponent field exactly then.
-__device__ __forceinline__ int block_exponent(uint32_t amax)
+// Returned as the bf16 bits of 2^(e + 8), which both the stored byte and 2^-e come from.
+__device__ __forceinline__ uint32_t block_exponent_bits(uint32_t amax)
 {
-    const int e = (int)((amax + 31u) >> 7) - (127 + 8);
-    return min(max(e, E_MIN), E_MAX);
+    const uint32_t lo = (uint32_t)(E_MIN + 8 + 127) << 7, hi = (uint32_t)(E_MAX + 8 + 127) << 7;
+    return min(max((amax + 31u) & 0xff80u, lo), hi);
 }
 
-// (code of lo, code of hi) in bits [0, 8) and [8, 16): nearest even, saturated to 448
-__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi)
+// codes of a, b, c, d from the lowest byte on: nearest even, saturated to 448
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d)
 {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    uint32_t r;
+    asm("{\n"
+        ".reg .b16 lo, hi;\n"
+        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n"
+        "mov.b32 %0, {lo, hi};\n"
+        "}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
     return r;
 }
 
