@@ -476,10 +476,10 @@ __device__ __forceinline__ uint4 from_codes(uint2 c, uint32_t scale_byte)
 {
     const uint32_t f = scale_bits(scale_byte) * 0x10001u, g = scale_rest_bits(scale_byte) * 0x10001u;
     uint4 r;
-    r.x = mul_bf16x2(mul_bf16x2(spread_codes(__byte_perm(c.x, 0, 0x1100)), f), g);
-    r.y = mul_bf16x2(mul_bf16x2(spread_codes(__byte_perm(c.x, 0, 0x3322)), f), g);
-    r.z = mul_bf16x2(mul_bf16x2(spread_codes(__byte_perm(c.y, 0, 0x1100)), f), g);
-    r.w = mul_bf16x2(mul_bf16x2(spread_codes(__byte_perm(c.y, 0, 0x3322)), f), g);
+    r.x = mul_bf16x2(mul_bf16x2(spread_codes<CODES_01>(c.x, c.x), f), g);
+    r.y = mul_bf16x2(mul_bf16x2(spread_codes<CODES_23>(c.x, c.x), f), g);
+    r.z = mul_bf16x2(mul_bf16x2(spread_codes<CODES_01>(c.y, c.y), f), g);
+    r.w = mul_bf16x2(mul_bf16x2(spread_codes<CODES_23>(c.y, c.y), f), g);
     return r;
 }
 

@@ -150,13 +150,22 @@ __device__ __forceinline__ uint2 load_codes8(const uint8_t *p)
     return v;
 }
 
-// Codes to bf16.  Each 16-bit half of x holds one code twice (byte permutation of the caller);
-// moving its exponent and mantissa to bf16's places gives the code's value times 2^(7 - 127),
-// e4m3 subnormals becoming bf16 subnormals, and the product with 2^(120 + e) is exact.
-__device__ __forceinline__ uint32_t spread_codes(uint32_t x)
+// Two codes to bf16, the byte permutation P of (a, b) naming each half's code and, with the bit
+// that repeats a byte's sign, the half's upper byte.  A shift by four then brings sign, exponent
+// and mantissa to bf16's places and the mask clears the other copies of the sign.  That is the
+// code's value times 2^(7 - 127), e4m3 subnormals becoming bf16 subnormals, and the product
+// with 2^(120 + e) is exact.
+template <uint32_t P>
+__device__ __forceinline__ uint32_t spread_codes(uint32_t a, uint32_t b)
 {
-    return (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
+    uint32_t x;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(x) : "r"(a), "r"(b), "n"(P));
+    return (x << 4) & 0x87f087f0u;
 }
+// codes 0, 1 and 2, 3 of a word; code J of each of two words
+constexpr uint32_t CODES_01 = 0x9180u, CODES_23 = 0xb3a2u;
+template <int J>
+constexpr uint32_t CODES_OF_TWO = 0xc480u + 0x1111u * J;
 
 // bf16 bits of 2^(120 + e); 2^127 for e > 7, the rest being scale_rest's
 __device__ __forceinline__ uint32_t scale_bits(uint32_t scale_byte)

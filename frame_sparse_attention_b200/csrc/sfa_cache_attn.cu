@@ -210,14 +210,11 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint4 &a, uint32_
         : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
-// The four codes of a word -> two bf16 pairs times f.  In bf16's place a code is its sign, then
-// four zero bits, then its other seven bits: the low bytes of the four halves and the high ones
-// are formed for the whole word and dealt out.
+// The four codes of a word -> two bf16 pairs times f
 __device__ __forceinline__ void codes_of_word(uint32_t w, uint32_t f, uint32_t &p0, uint32_t &p1)
 {
-    const uint32_t lo = (w << 4) & 0xf0f0f0f0u, hi = (w & 0x80808080u) | ((w >> 4) & 0x07070707u);
-    p0 = mul_bf16x2(__byte_perm(lo, hi, 0x5140), f);
-    p1 = mul_bf16x2(__byte_perm(lo, hi, 0x7362), f);
+    p0 = mul_bf16x2(spread_codes<CODES_01>(w, w), f);
+    p1 = mul_bf16x2(spread_codes<CODES_23>(w, w), f);
 }
 
 // compile-time answers for the code paths of large scales
@@ -530,8 +527,10 @@ __global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
                 uint32_t b[2][4];
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    codes_of_word(__byte_perm(v[2 * s][w], v[2 * s + 1][w], 0x5140), f[s], b[s][0], b[s][1]);
-                    codes_of_word(__byte_perm(v[2 * s][w], v[2 * s + 1][w], 0x7362), f[s], b[s][2], b[s][3]);
+                    b[s][0] = mul_bf16x2(spread_codes<CODES_OF_TWO<0>>(v[2 * s][w], v[2 * s + 1][w]), f[s]);
+                    b[s][1] = mul_bf16x2(spread_codes<CODES_OF_TWO<1>>(v[2 * s][w], v[2 * s + 1][w]), f[s]);
+                    b[s][2] = mul_bf16x2(spread_codes<CODES_OF_TWO<2>>(v[2 * s][w], v[2 * s + 1][w]), f[s]);
+                    b[s][3] = mul_bf16x2(spread_codes<CODES_OF_TWO<3>>(v[2 * s][w], v[2 * s + 1][w]), f[s]);
                     if (TWO) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) b[s][i] = mul_bf16x2(b[s][i], f2[s]);
