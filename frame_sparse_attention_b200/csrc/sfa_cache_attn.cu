@@ -37,6 +37,7 @@ struct ChunkArgs {
     int32_t *status;
     int32_t n_row_tiles, n_split;
     int32_t range_len;  // key steps of a range, see n_ranges
+    int32_t target;     // > 0: CTAs that the lengths on the device are dealt out to
     float *part_o;    // [n_split][B * H * Lq][d], normalised, when n_split > 1
     float *part_lse;  // [n_split][B * H * Lq], log2 units
     uint64_t timeout_ns;
@@ -51,6 +52,8 @@ struct ChunkArgs {
 // 764 us instead of 568.
 constexpr float GROWTH = 24.f;
 
+constexpr float EQUAL_LENGTHS = 0.93f;  // mean over longest, from which the caches count as equally long
+
 // What a CTA works on: rows [row0, row0 + tile) of (b, hk), row r being token r / G of query
 // head hk * G + r % G, and its share of the keys those rows see.
 struct Unit {
@@ -64,8 +67,14 @@ __device__ __forceinline__ Unit open_unit(const ChunkArgs &a, int tile_rows)
 {
     Unit u;
     int x = blockIdx.x;
-    u.split = x % a.n_split;
-    x /= a.n_split;
+    if (a.target) {  // the CTAs that may have no range of their own come last
+        const int units = gridDim.x / a.n_split;
+        u.split = x / units;
+        x -= u.split * units;
+    } else {
+        u.split = x % a.n_split;
+        x /= a.n_split;
+    }
     // causal: the last row tiles see the most keys and start first
     const int rt = x % a.n_row_tiles;
     u.row0 = (a.causal ? a.n_row_tiles - 1 - rt : rt) * tile_rows;
@@ -87,11 +96,32 @@ __device__ __forceinline__ int row_limit(const ChunkArgs &a, const Unit &u, int 
     return a.causal ? max(0, min(u.n, u.n - u.m + r / a.G + 1)) : u.n;
 }
 
-// Ranges that the key steps of a unit are cut into: as many of range_len steps as it has, so
-// that long and short caches give pieces of one length, but no more than the n_split CTAs
-// that it was given (caches longer than the caller's bound just get longer ranges).
-__device__ __forceinline__ int n_ranges(const ChunkArgs &a, int steps)
+// Ranges that the key steps of a unit are cut into (every lane of a warp calls it): as many of
+// range_len steps as it has, so that long and short caches give pieces of one length, but never
+// more than the n_split CTAs that it was given (caches longer than the caller's bound just get
+// longer ranges).
+// With a target, unless the lengths are nearly equal: its share of `target` ranges in all, by the
+// steps of all units, so that all the CTAs start at once and end together (one token, 8 x 12
+// units of 64 to 128 steps: 77 us, against 86 with ranges cut by the bound; at equal lengths 96
+// against 92, the shares being whole numbers).
+__device__ __forceinline__ int n_ranges(const ChunkArgs &a, int steps, int step_keys)
 {
+    if (a.target) {
+        const int heads = a.B * a.Hk;
+        int total = 0, longest = 0;
+        for (int x = threadIdx.x & 31; x < heads; x += 32) {
+            const int b = x / a.Hk, n = __ldg(a.kv_lens + b * a.ls0 + (x - b * a.Hk) * a.ls1);
+            const int t = n > 0 && n <= a.cache.table_len * a.cache.page_len ? (n + step_keys - 1) / step_keys : 0;
+            total += t;
+            longest = max(longest, t);
+        }
+        const float sum = (float)__reduce_add_sync(0xffffffffu, total);
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        if (sum < EQUAL_LENGTHS * longest * heads) {
+            const int share = (int)(steps * (a.target / (fmaxf(sum, 1.f) * a.n_row_tiles)) + 0.5f);
+            return max(1, min(min(a.n_split, steps), share));
+        }
+    }
     return max(1, min(a.n_split, (steps + a.range_len - 1) / a.range_len));
 }
 
@@ -296,7 +326,7 @@ __global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
     // the tile's last row sees the most keys
     const int seen = row_limit(a, u, min(u.row0 + FR_ROWS, u.n_rows) - 1);
     const int steps = (seen + FR_KEYS - 1) / FR_KEYS;
-    const int ranges = n_ranges(a, steps);
+    const int ranges = n_ranges(a, steps, FR_KEYS);
     if (u.split >= ranges) return skip_range(a, u, FR_ROWS);
     const int s0 = (int)((int64_t)steps * u.split / ranges), s1 = (int)((int64_t)steps * (u.split + 1) / ranges);
     // this warp's stretches: keys FR_KEYS (s0 + k) + 32 warp .. + 31, those that start before the end
@@ -1158,7 +1188,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1) tile_attn_kernel(const __grid_c
     if (u.row0 >= u.n_rows) return;
     const int seen = row_limit(a, u, min(u.row0 + CT_ROWS, u.n_rows) - 1);
     const int all = (seen + BN - 1) / BN;
-    const int ranges = n_ranges(a, all);
+    const int ranges = n_ranges(a, all, BN);
     if (u.split >= ranges) return skip_range(a, u, CT_ROWS);
     const int t0 = (int)((int64_t)all * u.split / ranges);
     const int n_tiles = (int)((int64_t)all * (u.split + 1) / ranges) - t0;
@@ -1294,11 +1324,13 @@ sfa_status check_attn(const sfa_cache_attn_desc *d)
 
 struct Plan {
     bool tiles;  // tile_attn_kernel, else rows_attn_kernel
-    int row_tiles, n_split, range_len;
+    int row_tiles, n_split, range_len, target;
     int64_t ctas;
 };
 
 constexpr int FEW_ROWS = 32;
+constexpr double DEALT_STEPS = 6.0;  // key steps a CTA, below which the lengths are not dealt out
+constexpr int MAX_DEALT = 1024;  // caches (B * H_kv) whose lengths every CTA reads
 
 // Which kernel.  Up to 32 query rows of a key head, 16 rows a CTA read the cache at most twice
 // and win (12 heads x 4 sequences over 8192 tokens, d = 128: 24 rows 56 against 61 us, 32 rows 57
@@ -1348,6 +1380,17 @@ Plan plan_of(const sfa_cache_attn_desc *d, const sfa_cache *c)
         }
     }
     p.range_len = (int)std::min<int64_t>((steps + p.n_split - 1) / p.n_split, 1 << 30);
+    // Few rows: uneven caches are better cut by their own lengths, into as many ranges as start
+    // at once less a few for the rounding (n_ranges), while that leaves a unit some four ranges
+    // and a range six steps at lengths of three quarters of the bound (five waves and 8 steps,
+    // 32 x 8 caches of 8192: 104 us cut by the bound, 116 by the lengths; one wave and 5 steps,
+    // 4 x 12 of 8192, d = 64: 21.2 and 23.3).  Twice the mean number of CTAs a unit: lengths up
+    // to twice the mean have ranges like the others.
+    p.target = 0;
+    if (!p.tiles && 4.0 * units <= slots && (int64_t)d->B * d->H_kv <= MAX_DEALT && 0.75 * units * steps >= DEALT_STEPS * slots) {
+        p.target = (int)(0.96 * slots);
+        p.n_split = (int)std::min<int64_t>(std::min<int64_t>(MAX_SPLIT, steps), 2 * ((p.target + units - 1) / units));
+    }
     p.ctas = units * p.n_split;
     return p;
 }
@@ -1472,6 +1515,7 @@ extern "C" sfa_status sfa_forward_cache(const sfa_cache_attn_desc *d, const sfa_
     a.part_o = static_cast<float *>(workspace);
     a.part_lse = a.part_o ? a.part_o + (int64_t)p.n_split * rows * d->d : nullptr;
     a.range_len = p.range_len;
+    a.target = p.target;
     a.timeout_ns = (uint64_t)(d->timeout_us ? d->timeout_us : DEFAULT_TIMEOUT_US) * 1000;
     a.debug_flags = d->debug_flags;
     cudaStream_t s = as_cuda(stream);

@@ -50,7 +50,7 @@ def poisoned(m, cache, table, lens, per_head):
 
 
 def run_case(B, H, Hk, L, d, P, kv, per_head=False, causal=False, ragged=False, q_ragged=False, mem="bhld", seed=0,
-             scale=None, max_kv=None, q_gain=1.0, flags=0):
+             scale=None, max_kv=None, q_gain=1.0, flags=0, table_len=0):
     m, g = sfa(), np.random.default_rng(seed + 7 * L + kv + d)
     heads, rows = (1, Hk) if per_head else (Hk, 1)
     n = max(1, -(-kv // P))
@@ -65,6 +65,8 @@ def run_case(B, H, Hk, L, d, P, kv, per_head=False, causal=False, ragged=False, 
     if not per_head:
         lens[:] = lens[:, :1]
     poisoned(m, cache, table, lens, per_head)
+    if table_len > n:  # a table that could hold far more than it does
+        table = np.concatenate([table, np.zeros((B, rows, table_len - n), np.int32)], 2)
     q_lens = None
     if q_ragged:
         q_lens = g.integers(0, L + 1, B).astype(np.int32)
@@ -76,7 +78,7 @@ def run_case(B, H, Hk, L, d, P, kv, per_head=False, causal=False, ragged=False, 
     out = strided(torch.full_like(q, 5.0).cuda(), mem)
     lse = torch.full((B, H, L), 5.0, device="cuda")
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    args = dict(causal=causal, scale=scale, max_kv=kv if max_kv is None else max_kv, H_kv=Hk, debug_flags=flags,
+    args = dict(causal=causal, scale=scale, max_kv=(0 if table_len else kv) if max_kv is None else max_kv, H_kv=Hk, debug_flags=flags,
                 q_lens=None if q_lens is None else torch.from_numpy(q_lens).cuda())
     t, ln = torch.from_numpy(table).cuda(), torch.from_numpy(lens if per_head else lens[:, 0].copy()).cuda()
     o, l = m.forward_cache(qc, cache, t, ln, out=out, lse=lse, dev_status=status, **args)
@@ -118,6 +120,39 @@ ROWS, TILES = 4, 8  # SFA_DEBUG_CACHE_*: the kernel of few rows, the kernel of m
 @pytest.mark.parametrize("case", SMALL, ids=lambda c: "B{B}H{H}.{Hk}L{L}d{d}P{P}kv{kv}".format(**c))
 def test_few_rows(case, flags):
     run_case(**case, flags=flags)
+
+
+# Tables long enough that the few rows' ranges are cut by the lengths on the device
+DEALT = [
+    dict(B=3, H=4, Hk=2, L=1, d=128, P=64, kv=2000, ragged=True, per_head=True, table_len=1300),
+    dict(B=2, H=9, Hk=3, L=6, d=64, P=40, kv=900, ragged=True, causal=True, q_ragged=True, table_len=2000),
+    dict(B=5, H=5, Hk=5, L=1, d=64, P=16, kv=3000, ragged=True, table_len=6000),
+    dict(B=2, H=2, Hk=2, L=17, d=128, P=7, kv=131, ragged=True, per_head=True, table_len=20000),
+    dict(B=4, H=8, Hk=4, L=1, d=128, P=64, kv=1500, table_len=600),
+    dict(B=2, H=4, Hk=2, L=2, d=128, P=64, kv=0, table_len=2000),
+    dict(B=1, H=2, Hk=1, L=3, d=64, P=64, kv=50, table_len=8000),
+]
+
+
+@pytest.mark.parametrize("case", DEALT, ids=lambda c: "B{B}H{H}.{Hk}L{L}d{d}P{P}kv{kv}".format(**c))
+def test_ranges_cut_by_the_lengths(case):
+    m, q, cache, t, ln, o, l, args = run_case(**case)
+    # a captured call cuts them by the lengths that it finds
+    graph = torch.cuda.CUDAGraph()
+    out, lse = torch.zeros_like(o), torch.zeros_like(l)
+    ws = torch.empty(m.forward_cache_workspace_bytes(q, cache, t, ln, max_kv=args["max_kv"], H_kv=args["H_kv"]),
+                     dtype=torch.uint8, device="cuda")
+    kept = ln.clone()
+    ln.zero_()
+    with torch.cuda.graph(graph):
+        m.forward_cache(q, cache, t, ln, out=out, lse=lse, workspace=ws, **args)
+    graph.replay()
+    ln.copy_(kept)
+    graph.replay()
+    torch.cuda.synchronize()
+    for b in range(case["B"]):
+        n = case["L"] if args["q_lens"] is None else int(args["q_lens"][b])
+        assert torch.equal(out[b, :, :n], o[b, :, :n]) and torch.equal(lse[b, :, :n], l[b, :, :n])
 
 
 CHUNKS = [
