@@ -119,6 +119,17 @@ def _launch(dev, fn, args, stream, what):
         raise SfaError(status, what)
 
 
+def _new(make, *args, stream, dev, **kw):
+    """make(*args, **kw) for a call on ``stream``: what is allocated here belongs to that stream,
+    whose order a fill and a later reuse of the memory then follow."""
+    if stream is None:
+        return make(*args, **kw)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
 def _rows(name, t, dev, shape):
     """(strides, address) of a bf16 tensor of this shape."""
     if t.dtype is not _BF16 or t.get_device() != dev or t.shape != shape:
@@ -235,13 +246,13 @@ def qk_norm_rope(q, k=None, rope: RopeTable | None = None, positions=None, q_wei
         shape = q.shape
         H = shape[1]
         sq, qp = _rows("q", q, dev, shape)
-        q_out = torch.empty_like(q) if q_out is None else q_out
+        q_out = _new(torch.empty_like, q, stream=stream, dev=dev) if q_out is None else q_out
         so, qop = _rows("q_out", q_out, dev, shape)
     if k is not None:
         H_kv = _shape4("k", k)[1]
         shape = (B, H_kv, L, d)
         sk, kp = _rows("k", k, dev, shape)
-        k_out = torch.empty_like(k) if k_out is None else k_out
+        k_out = _new(torch.empty_like, k, stream=stream, dev=dev) if k_out is None else k_out
         sko, kop = _rows("k_out", k_out, dev, shape)
     desc = _ROWS.pack(B, H, H_kv, L, d, -1.0 if eps is None else eps, *sq, *sk, *_NO, *so, *sko, *_NO, 0, 0)
     _launch(dev, load().sfa_qk_norm_rope,
@@ -280,7 +291,7 @@ def cache_append(cache: FrameCache, q, k, v, table, start, lens=None, rope: Rope
     sq, qp = _rows("q", q, dev, shape)
     sk, kp = _rows("k", k, dev, kv_shape)
     sv, vp = _rows("v", v, dev, kv_shape)
-    q_out = torch.empty_like(q) if q_out is None else q_out
+    q_out = _new(torch.empty_like, q, stream=stream, dev=dev) if q_out is None else q_out
     so, qop = _rows("q_out", q_out, dev, shape)
     cd = _cache_desc(cache, table, dev, B, H_kv, d)
     desc = _ROWS.pack(B, H, H_kv, L, d, -1.0 if eps is None else eps, *sq, *sk, *sv, *so, *_NO, *_NO,
@@ -303,9 +314,9 @@ def cache_read(cache: FrameCache, table, start, L: int, lens=None, k_out=None, v
         H_kv = _shape4("k_out", k_out)[1] if k_out is not None else max(pool[1], t[1] if len(t) == 3 else 1)
     shape = (B, H_kv, int(L), d)
     if k_out is None:
-        k_out = torch.zeros(shape, dtype=_BF16, device=cache.k.device)
+        k_out = _new(torch.zeros, shape, dtype=_BF16, device=cache.k.device, stream=stream, dev=dev)
     if v_out is None:
-        v_out = torch.zeros(shape, dtype=_BF16, device=cache.k.device)
+        v_out = _new(torch.zeros, shape, dtype=_BF16, device=cache.k.device, stream=stream, dev=dev)
     sk, kp = _rows("k_out", k_out, dev, shape)
     sv, vp = _rows("v_out", v_out, dev, shape)
     cd = _cache_desc(cache, table, dev, B, H_kv, d)
@@ -355,11 +366,11 @@ def forward_cache(q, cache: FrameCache, table, kv_lens, causal: bool = False, q_
     dev = q.get_device()
     shape = _shape4("q", q)
     sq, qp = _rows("q", q, dev, shape)
-    out = torch.empty_like(q) if out is None else out
+    out = _new(torch.empty_like, q, stream=stream, dev=dev) if out is None else out
     so, op = _rows("out", out, dev, shape)
     B, H, Lq, d = shape
     if lse is None:
-        lse = torch.empty(shape[:3], dtype=_F32, device=q.device)
+        lse = _new(torch.empty, shape[:3], dtype=_F32, device=q.device, stream=stream, dev=dev)
     elif lse.dtype is not _F32 or lse.get_device() != dev or lse.shape != shape[:3] or not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous fp32 tensor {tuple(shape[:3])} on device {dev}")
     if H_kv is None:
@@ -372,7 +383,7 @@ def forward_cache(q, cache: FrameCache, table, kv_lens, causal: bool = False, q_
         need = ctypes.c_size_t(0)
         _check(lib.sfa_forward_cache_workspace(desc, cd, ctypes.byref(need)), "sfa_forward_cache_workspace")
         if need.value:
-            workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
+            workspace = _new(torch.empty, need.value, dtype=torch.uint8, device=q.device, stream=stream, dev=dev)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on device {dev}")
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())

@@ -376,3 +376,31 @@ def test_the_choice_of_kernel_by_size():
     for L, B in ((31, 1), (32, 2), (33, 1), (40, 5)):
         run_case(B=B, H=4, Hk=4, L=L, d=64, P=32, kv=1100, ragged=True)
     run_case(B=2, H=6, Hk=6, L=130, d=128, P=64, kv=1400, per_head=True, causal=True)
+
+
+def test_what_a_call_allocates_follows_its_stream():
+    """Neither the zero fill of cache_read's outputs nor a reuse of forward_cache's workspace may
+    be ordered by another stream than the call's."""
+    m, g = sfa(), np.random.default_rng(5)
+    cache = random_pool(g, m, 40, 2, 64, 64)
+    table = torch.arange(40, dtype=torch.int32, device="cuda").reshape(1, 40)
+    lens = torch.tensor([2500], dtype=torch.int32, device="cuda")
+    start = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = torch.from_numpy(g.standard_normal((1, 2, 1, 64))).bfloat16().cuda()
+    k0, v0 = m.cache_read(cache, table, start, 300)
+    o0, l0 = m.forward_cache(q, cache, table, lens)
+    need = m.forward_cache_workspace_bytes(q, cache, table, lens)
+    assert need > 0
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        torch.cuda._sleep(20_000_000)  # the current stream is behind
+        k1, v1 = m.cache_read(cache, table, start, 300, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(k1, k0) and torch.equal(v1, v0)
+        with torch.cuda.stream(side):  # and now the other one
+            torch.cuda._sleep(20_000_000)
+        o1, l1 = m.forward_cache(q, cache, table, lens, stream=stream)
+        others = [torch.full((n,), 0xff, dtype=torch.uint8, device="cuda") for n in (need, need, need)]
+        torch.cuda.synchronize()
+        assert torch.equal(o1, o0) and torch.equal(l1, l0) and all((x == 0xff).all() for x in others)
