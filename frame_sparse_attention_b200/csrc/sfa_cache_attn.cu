@@ -647,8 +647,9 @@ __global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[j] = fmaf(c, src[j], acc[j]);
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const float lse2 = l > 0.f ? M + log2f(l) : -INFINITY;
+        // (a NaN, from a query that holds one, stays a NaN)
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        const float lse2 = l != 0.f ? M + log2f(l) : -INFINITY;
         const int64_t id = row_id(a, u, row);
         if (a.n_split == 1) {
             const int tok = row / a.G, h = u.hk * a.G + (row - tok * a.G);
@@ -1112,8 +1113,9 @@ __device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *s
     if (lane == 0) epi_ok[warp] = have ? 1 : 0;
     named_bar_sync(1 + x, BM);
     if (!(epi_ok[0] && epi_ok[1] && epi_ok[2] && epi_ok[3])) return;  // uniform over the tile's warps
-    const float inv_l = l > 0.f ? 1.f / l : 0.f;
-    const float lse2 = l > 0.f ? m_used + log2f(l) : -INFINITY;
+    // (a NaN, from a query that holds one, stays a NaN)
+    const float inv_l = l != 0.f ? 1.f / l : 0.f;
+    const float lse2 = l != 0.f ? m_used + log2f(l) : -INFINITY;
     const bool there = r < u.n_rows;
     const int64_t part_rows = (int64_t)a.B * a.H * a.Lq;
     if (n_tiles > 0) tc_fence_after();
@@ -1293,14 +1295,14 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
 #pragma unroll
             for (int j = 0; j < E; ++j) acc[j] = fmaf(w[k], x[k][j], acc[j]);
     }
-    const float inv = total > 0.f ? 1.f / total : 0.f;
+    const float inv = total != 0.f ? 1.f / total : 0.f;
     uint16_t *dst = a.o + b * a.os[0] + h * a.os[1] + i * a.os[2] + lane * E;
     if (E == 4)
         *reinterpret_cast<uint2 *>(dst) =
             make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[E - 2] * inv, acc[E - 1] * inv));
     else
         *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    if (lane == 0) a.lse[id] = total > 0.f ? (M + log2f(total)) * 0.69314718055994530942f : -INFINITY;
+    if (lane == 0) a.lse[id] = total != 0.f ? (M + log2f(total)) * 0.69314718055994530942f : -INFINITY;
 }
 
 // ----------------------------------------------------------------- host side

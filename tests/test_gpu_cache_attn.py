@@ -404,3 +404,21 @@ def test_what_a_call_allocates_follows_its_stream():
         others = [torch.full((n,), 0xff, dtype=torch.uint8, device="cuda") for n in (need, need, need)]
         torch.cuda.synchronize()
         assert torch.equal(o1, o0) and torch.equal(l1, l0) and all((x == 0xff).all() for x in others)
+
+
+@pytest.mark.parametrize("flags", [ROWS, TILES])
+@pytest.mark.parametrize("L,kv", [(3, 90), (3, 6000), (150, 700)])
+def test_a_query_with_nan_answers_nan(L, kv, flags):
+    """In its own row and no other, with the keys in one range and in several."""
+    m, g = sfa(), np.random.default_rng(kv)
+    cache = random_pool(g, m, 100, 1, 64, 64)
+    table = g.permutation(100).astype(np.int32).reshape(1, 1, 100)
+    q = torch.from_numpy(g.standard_normal((1, 1, L, 64))).bfloat16()
+    q[0, 0, 1, 5] = float("nan")
+    o, l = m.forward_cache(q.cuda(), cache, torch.from_numpy(table).cuda(),
+                           torch.tensor([kv], dtype=torch.int32, device="cuda"), debug_flags=flags)
+    torch.cuda.synchronize()
+    assert torch.isnan(o[0, 0, 1]).all() and torch.isnan(l[0, 0, 1])
+    rest = [i for i in range(L) if i != 1]
+    k, v = gather(cache, table, 0, 0, kv)
+    check(o[0, 0, rest], l[0, 0, rest], f64(q[0, 0, rest]), k, v, 0.125, False)
