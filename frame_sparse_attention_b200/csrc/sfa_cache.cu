@@ -640,6 +640,13 @@ sfa_status check_cache_rows(const sfa_rows_desc *d, const sfa_cache *cache, cons
     return SFA_OK;
 }
 
+// Pages of one head each, one row of them for all heads and one start: every head would be
+// written to the same places.
+bool heads_collide(const sfa_rows_desc *d, const sfa_cache *c)
+{
+    return c->heads == 1 && d->H_kv > 1 && c->table_stride[1] == 0 && d->start_stride[1] == 0;
+}
+
 }  // namespace
 }  // namespace sfa
 
@@ -690,7 +697,7 @@ extern "C" sfa_status sfa_cache_write(const sfa_rows_desc *d, const sfa_cache *c
     if (d->B == 0 || d->L == 0) return SFA_OK;
     st = check_cache_rows(d, cache, start);
     if (st != SFA_OK) return st;
-    if (!k || !v || !aligned16(k) || !aligned16(v)) return SFA_ERR_INVALID_ARG;
+    if (!k || !v || !aligned16(k) || !aligned16(v) || heads_collide(d, cache)) return SFA_ERR_INVALID_ARG;
     if (!rows_stride_ok(d->k_stride, d->B, d->H_kv, d->L) || !rows_stride_ok(d->v_stride, d->B, d->H_kv, d->L))
         return SFA_ERR_INVALID_ARG;
     RowsArgs a = {};
@@ -720,7 +727,7 @@ extern "C" sfa_status sfa_cache_append(const sfa_rows_desc *d, const sfa_rope *r
     if (d->B == 0 || d->L == 0) return SFA_OK;
     st = check_cache_rows(d, cache, start);
     if (st != SFA_OK) return st;
-    if (!q || !k || !v || !q_out || !heads_ok(d->H)) return SFA_ERR_INVALID_ARG;
+    if (!q || !k || !v || !q_out || !heads_ok(d->H) || heads_collide(d, cache)) return SFA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !weights_ok(q_weight, k_weight))
         return SFA_ERR_INVALID_ARG;
     if (!rows_stride_ok(d->q_stride, d->B, d->H, d->L) || !rows_stride_ok(d->q_out_stride, d->B, d->H, d->L) ||

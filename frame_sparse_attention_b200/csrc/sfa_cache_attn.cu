@@ -111,7 +111,8 @@ __device__ __forceinline__ int n_ranges(const ChunkArgs &a, int steps, int step_
         int total = 0, longest = 0;
         for (int x = threadIdx.x & 31; x < heads; x += 32) {
             const int b = x / a.Hk, n = __ldg(a.kv_lens + b * a.ls0 + (x - b * a.Hk) * a.ls1);
-            const int t = n > 0 && n <= a.cache.table_len * a.cache.page_len ? (n + step_keys - 1) / step_keys : 0;
+            // (cut at 2^20 so that 1024 of them add up in 32 bits)
+            const int t = n > 0 && n <= a.cache.table_len * a.cache.page_len ? min((n + step_keys - 1) / step_keys, 1 << 20) : 0;
             total += t;
             longest = max(longest, t);
         }
@@ -1318,7 +1319,7 @@ sfa_status check_attn(const sfa_cache_attn_desc *d)
     if (!d || d->B < 0 || d->Lq < 0 || d->max_kv < 0) return SFA_ERR_INVALID_ARG;
     if (d->d != 64 && d->d != 128) return SFA_ERR_UNSUPPORTED;
     if (d->H < 1 || d->H > SFA_MAX_HEADS || d->H_kv < 1 || d->H % d->H_kv) return SFA_ERR_INVALID_ARG;
-    if (!(d->scale > 0.f) || !std::isfinite(d->scale)) return SFA_ERR_INVALID_ARG;
+    if (!(d->scale > 0.f) || !std::isfinite(d->scale * 1.4426950408889634f)) return SFA_ERR_INVALID_ARG;
     if (d->len_stride[0] < 0 || d->len_stride[1] < 0) return SFA_ERR_INVALID_ARG;
     if ((int64_t)d->B * d->H * d->Lq >= ((int64_t)1 << 31)) return SFA_ERR_INVALID_ARG;
     return SFA_OK;

@@ -544,6 +544,7 @@ typedef struct {
  * Norm and rotation of queries and keys in one pass:
  *   y = x / sqrt(mean(x^2) + eps) * weight  (per head row; weight fp32 [d], 16-byte aligned,
  *   or NULL = ones; no norm with eps < 0), then the rotation (rope NULL: none), in fp32, rounded to bf16 once.
+ *   (The sum of squares is fp32 too: rows whose elements pass 1e19 give 0.)
  * q or k may be NULL (with its output).  q_out / k_out may be q / k themselves (same strides).
  */
 sfa_status sfa_qk_norm_rope(const sfa_rows_desc *desc, const sfa_rope *rope, const void *q, const void *k,
@@ -555,8 +556,9 @@ sfa_status sfa_qk_norm_rope(const sfa_rows_desc *desc, const sfa_rope *rope, con
  *   start  device int32 (strides in the descriptor).
  *   lens   device int32 [B] or NULL (= L): rows i >= lens[b] are skipped (padded batches).
  * A token whose place lies outside the table, or whose page number outside the pool, is
- * skipped and reported as SFA_ERR_BAD_SET in dev_status.  Two tokens with the same place:
- * either may win, per 8 elements.
+ * skipped and reported as SFA_ERR_BAD_SET in dev_status.  Tokens of one call with the same place
+ * leave that row unspecified; pages of one head each under a table row and a start that H_kv > 1
+ * heads share, where all of them would meet, are SFA_ERR_INVALID_ARG.
  */
 sfa_status sfa_cache_write(const sfa_rows_desc *desc, const sfa_cache *cache, const void *k, const void *v,
                            const int32_t *start, const int32_t *lens, int32_t *dev_status, sfa_stream_t stream);
@@ -594,11 +596,12 @@ sfa_status sfa_cache_read(const sfa_rows_desc *desc, const sfa_cache *cache, con
  * [0, table_len * page_len] or a page number outside the pool is reported as
  * SFA_ERR_BAD_SET in dev_status; the rows of that (b, hk) are then unspecified, and nothing
  * outside the pool is read.  Scores, softmax and partial results are fp32; the
- * probabilities are rounded to bf16 for the product with V, as in sfa_forward.
+ * probabilities are rounded to bf16 for the product with V, as in sfa_forward.  Values of 2^100
+ * and more may overflow in a partial result.  A query that holds a NaN answers NaN.
  */
 typedef struct {
     int32_t B, H, H_kv, Lq, d;
-    float scale;               /* > 0, finite                                              */
+    float scale;               /* > 0; scale * log2(e) finite                              */
     int32_t causal;
     int32_t max_kv;
     int64_t q_stride[3], o_stride[3]; /* batch, head, token                                */

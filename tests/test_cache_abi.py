@@ -138,6 +138,16 @@ def test_start(sfa, fn):
     assert _call(sfa, fn, rows, cache, rope) == 1
 
 
+@pytest.mark.parametrize("fn", ("write", "append"))
+def test_heads_that_would_meet_in_one_place(sfa, fn):
+    rows, cache, rope = _structs()
+    cache.heads = 1
+    cache.table_stride_h = 0
+    assert _call(sfa, fn, rows, cache, rope) == 1
+    rows.H_kv, rows.B = 1, 0  # (nothing to do, so that nothing is launched)
+    assert _call(sfa, fn, rows, cache, rope) == 0
+
+
 @pytest.mark.parametrize("over,pairs,code", [
     (dict(inv_freq=None), (16,), 1), (dict(positions=None), (16,), 1), (dict(inv_freq=GOOD + 4), (16,), 1),
     (dict(positions=GOOD + 2), (16,), 1), (dict(layout=2), (16,), 1), (dict(n_axes=0), (), 1), (dict(n_axes=5), (), 1),
@@ -235,7 +245,7 @@ def _attn_call(sfa, d, cache, q=GOOD, o=GOOD, lse=GOOD, lens=GOOD, ws=None, ws_b
 
 @pytest.mark.parametrize("over,code", [(dict(B=-1), 1), (dict(Lq=-1), 1), (dict(d=96), 2), (dict(H=0), 1), (dict(H=3), 1),
                                        (dict(H_kv=0), 1), (dict(H_kv=4), 1), (dict(scale=0.0), 1), (dict(scale=-1.0), 1),
-                                       (dict(scale=float("inf")), 1), (dict(max_kv=-1), 1), (dict(len_stride_b=-1), 1),
+                                       (dict(scale=float("inf")), 1), (dict(scale=3e38), 1), (dict(max_kv=-1), 1), (dict(len_stride_b=-1), 1),
                                        (dict(q_stride1=12), 1), (dict(o_stride2=0), 1), (dict(d=128), 1)])
 def test_attention_descriptor(sfa, over, code):
     _, cache, _ = _structs()

@@ -297,6 +297,10 @@ APPEND_CASES = [
     (3, 6, 2, 1, 64, 16, False, False, "half", (32,)),
     (2, 6, 3, 41, 128, 7, True, True, "interleaved", (44, 42, 42)),
     (1, 12, 12, 333, 64, 40, True, False, "interleaved", (22,)),
+    (2, 80, 40, 33, 64, 16, False, True, "half", (48,)),
+    # a warp for every token, and more heads than it looks up at a time
+    (2, 40, 40, 1250, 64, 16, False, True, "half", (64,)),
+    (1, 2, 35, 2400, 128, 24, True, False, "interleaved", (64, 32)),
 ]
 
 
