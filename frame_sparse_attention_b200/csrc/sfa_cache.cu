@@ -57,7 +57,8 @@ struct RowsArgs {
     const int32_t *lens;
     int32_t *status;
     int32_t n_parts;   // warps per token
-    uint32_t n_warps;  // B * L * n_parts
+    uint32_t tokens;   // B * L
+    uint32_t n_warps;  // tiles of tokens * n_parts
     uint32_t rows;     // B * Hk * L
 };
 
@@ -309,54 +310,64 @@ struct HeadRows {
     }
 };
 
-// One warp per token, or one of n_parts warps that share a token's row groups: groups
-// [0, Gq) are the query heads, [Gq, Gq + Gk) the key (and value) heads, RW heads a group,
-// and part p takes the groups g = p mod n_parts.  The loads of the first U groups go out
-// before the angles are formed, and a group's registers are loaded again as soon as it is
-// done, so a warp has rows under way throughout.  With the cache, a lane looks up the place of
-// one of the part's key rows before any is stored.
-template <int D, bool HALF, bool CACHE>
+// A warp takes a token, or with MANY RW consecutive tokens of the (b, i) order (RW rows at a time,
+// D / 8 lanes to a row); where tokens are few, n_parts warps share them.  A group is RW heads of the
+// token, or one head of each of the tokens: groups [0, Gq) are the queries', [Gq, Gq + Gk) the
+// keys' (and values'), and part p takes the groups g = p mod n_parts.  The angles are formed once
+// for all heads.  The loads of the first U groups go out before them, and a group's registers are
+// loaded again as soon as it is done, so a warp has rows under way throughout.  With the cache,
+// a lane looks up the place of one of the part's key rows before any is stored.
+template <int D, bool HALF, bool CACHE, bool MANY>
 __global__ void __launch_bounds__(ROW_WARPS * 32, ROW_CTAS) rows_kernel(const __grid_constant__ RowsArgs a)
 {
     constexpr int G = D / 8;     // lanes per row
-    constexpr int RW = 32 / G;   // rows of a group
-    constexpr int U = CACHE ? 2 : 4;  // groups under way (append, U = 4: 31 against 29 us)
-    __shared__ __align__(16) float cos_all[ROW_WARPS][D / 2], sin_all[ROW_WARPS][D / 2];
+    constexpr int RW = ROWS_AT_ONCE<D>;
+    constexpr int T = MANY ? RW : 1;  // tokens
+    constexpr int U = CACHE ? 2 : 4;  // query groups under way (append, U = 4: 31 against 29 us)
+    __shared__ __align__(16) float cos_all[ROW_WARPS][T][D / 2], sin_all[ROW_WARPS][T][D / 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t w = blockIdx.x * (uint32_t)ROW_WARPS + warp;
     if (w >= a.n_warps) return;
-    const uint32_t token = a.n_parts == 1 ? w : w / (uint32_t)a.n_parts;
-    const int part = (int)(w - token * a.n_parts);
-    const int b = (int)(token / (uint32_t)a.L), i = (int)(token - b * (uint32_t)a.L);
-    if (a.lens && i >= __ldg(a.lens + b)) return;  // a padded row (the whole warp)
+    const uint32_t tile = a.n_parts == 1 ? w : w / (uint32_t)a.n_parts;
+    const int part = (int)(w - tile * a.n_parts);
     const int sub = lane / G, e0 = (lane % G) * 8;
-    const int Gq = a.q ? (a.H + RW - 1) / RW : 0;
-    const int Gk = a.k ? (a.Hk + RW - 1) / RW : 0;
+    // this lane's token; want: it is one, and not a padded row
+    const uint32_t token = tile * T + (MANY ? sub : 0), at = MANY ? min(token, a.tokens - 1) : token;
+    const int b = (int)(at / (uint32_t)a.L), i = (int)(at - b * (uint32_t)a.L);
+    const bool want = token < a.tokens && !(a.lens && i >= __ldg(a.lens + b));
+    if (!__any_sync(0xffffffffu, want)) return;
+    auto groups = [](int heads) { return MANY ? heads : (heads + RW - 1) / RW; };
+    auto head = [&](int g) { return MANY ? g : g * RW + sub; };
+    const int Gq = a.q ? groups(a.H) : 0, Gk = a.k ? groups(a.Hk) : 0;
+    const int Hq = want ? a.H : 0, Hk = want ? a.Hk : 0;  // this lane's heads
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     const int step = a.n_parts;
 
     const uint16_t *q_src = a.q + b * a.qs[0] + i * a.qs[2] + e0;
     auto load_q = [&](int g) {
-        const int h = g * RW + sub;
-        return g < Gq && h < a.H ? *reinterpret_cast<const uint4 *>(q_src + h * a.qs[1]) : zero;
+        const int h = head(g);
+        return g < Gq && h < Hq ? *reinterpret_cast<const uint4 *>(q_src + h * a.qs[1]) : zero;
     };
     const uint16_t *k_src = a.k + b * a.ks[0] + i * a.ks[2] + e0;
     auto load_k = [&](int g) {
-        const int h = g * RW + sub;
-        return g < Gk && h < a.Hk ? *reinterpret_cast<const uint4 *>(k_src + h * a.ks[1]) : zero;
+        const int h = head(g);
+        return g < Gk && h < Hk ? *reinterpret_cast<const uint4 *>(k_src + h * a.ks[1]) : zero;
     };
     // this part's first key group: g + Gq = part mod n_parts
     const int first = (part + step - Gq % step) % step;
-    // The cache rows of G of its groups from the m0-th on, one of their rows per lane: where the
-    // sequence starts, then the row (or -1).
+    // The cache rows of G of its groups from the m0-th on, one of their rows per lane, that of
+    // the lanes of sub = lane % RW: where the sequence starts, then the row (or -1).
+    const int b_row = MANY ? __shfl_sync(0xffffffffu, b, lane % RW * G) : b;
+    const int i_row = MANY ? __shfl_sync(0xffffffffu, i, lane % RW * G) : i;
+    const int Hk_row = MANY ? __shfl_sync(0xffffffffu, Hk, lane % RW * G) : Hk;
     auto my_head = [&](int m0) {
-        const int g = first + (m0 + lane / RW) * step, h = g * RW + lane % RW;
-        return g < Gk && h < a.Hk ? h : -1;
+        const int g = first + (m0 + lane / RW) * step, h = MANY ? g : g * RW + lane % RW;
+        return g < Gk && h < Hk_row ? h : -1;
     };
-    auto my_start = [&](int h) { return h < 0 ? 0 : __ldg(a.start + b * a.ss0 + h * a.ss1); };
+    auto my_start = [&](int h) { return h < 0 ? 0 : __ldg(a.start + b_row * a.ss0 + h * a.ss1); };
     auto my_row = [&](int h, int start) {
         if (h < 0) return -1;
-        const int row = (int)cache_row(a.cache, b, h, (int64_t)start + i);
+        const int row = (int)cache_row(a.cache, b_row, h, (int64_t)start + i_row);
         if (row < 0) report_status(a.status, SFA_ERR_BAD_SET);
         return row;
     };
@@ -365,14 +376,18 @@ __global__ void __launch_bounds__(ROW_WARPS * 32, ROW_CTAS) rows_kernel(const __
     for (int u = 0; u < U; ++u) x[u] = load_q(part + u * step);
     const int start0 = CACHE ? my_start(my_head(0)) : 0;
 
-    float *cosp = cos_all[warp], *sinp = sin_all[warp];
-    const int32_t *pos = a.R ? a.pos + b * a.ps0 + i * a.ps1 : nullptr;
-    for (int p = lane; p < D / 2; p += 32) {
-        const float2 r = p < a.R / 2 ? rotation(a, pos, p) : make_float2(1.f, 0.f);
-        cosp[p] = r.x;
-        sinp[p] = r.y;
+#pragma unroll 1
+    for (int t = 0; t < T; ++t) {
+        const int64_t bt = MANY ? __shfl_sync(0xffffffffu, b, t * G) : b, it = MANY ? __shfl_sync(0xffffffffu, i, t * G) : i;
+        const int32_t *pos = a.R ? a.pos + bt * a.ps0 + it * a.ps1 : nullptr;
+        for (int p = lane; p < D / 2; p += 32) {
+            const float2 r = p < a.R / 2 ? rotation(a, pos, p) : make_float2(1.f, 0.f);
+            cos_all[warp][t][p] = r.x;
+            sin_all[warp][t][p] = r.y;
+        }
     }
     __syncwarp();
+    const float *cosp = cos_all[warp][MANY ? sub : 0], *sinp = sin_all[warp][MANY ? sub : 0];
 
     Coef f;
     if (part < Gq) {
@@ -381,11 +396,11 @@ __global__ void __launch_bounds__(ROW_WARPS * 32, ROW_CTAS) rows_kernel(const __
         for (int g0 = part; g0 < Gq; g0 += U * step) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int g = g0 + u * step, h = g * RW + sub;
+                const int g = g0 + u * step, h = head(g);
                 if (g >= Gq) break;
                 const uint4 y = norm_rotate<D, HALF>(x[u], f, a.eps, e0, a.R);
                 x[u] = load_q(g + U * step);
-                if (h < a.H) *reinterpret_cast<uint4 *>(dst + h * a.qo[1]) = y;
+                if (h < Hq) *reinterpret_cast<uint4 *>(dst + h * a.qo[1]) = y;
             }
         }
     }
@@ -398,17 +413,17 @@ __global__ void __launch_bounds__(ROW_WARPS * 32, ROW_CTAS) rows_kernel(const __
         for (int g0 = first; g0 < Gk; g0 += U * step) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int g = g0 + u * step, h = g * RW + sub;
+                const int g = g0 + u * step, h = head(g);
                 if (g >= Gk) break;
                 const uint4 y = norm_rotate<D, HALF>(x[u], f, a.eps, e0, a.R);
                 x[u] = load_k(g + U * step);
-                if (h < a.Hk) *reinterpret_cast<uint4 *>(dst + h * a.ko[1]) = y;
+                if (h < Hk) *reinterpret_cast<uint4 *>(dst + h * a.ko[1]) = y;
             }
         }
     } else {
         coefficients<D, HALF>(f, cosp, sinp, a.k_weight, e0, a.R);
-        HeadRows k(a.k, b, first * RW + sub, i, e0, step * RW, a.ks, a.Hk);
-        HeadRows v(a.v, b, first * RW + sub, i, e0, step * RW, a.vs, a.Hk);
+        HeadRows k(a.k, b, head(first), i, e0, MANY ? step : step * RW, a.ks, Hk);
+        HeadRows v(a.v, b, head(first), i, e0, MANY ? step : step * RW, a.vs, Hk);
         uint4 kk = k.load(), vv = v.load();
         for (int m0 = 0; first + m0 * step < Gk; m0 += G) {
             const int mine = my_head(m0), row = my_row(mine, m0 ? my_start(mine) : start0);
@@ -593,27 +608,43 @@ void fill_rope(RowsArgs &a, const sfa_rope *r)
     a.R = 2 * pairs;
 }
 
-template <bool CACHE>
+template <bool CACHE, bool MANY>
 sfa_status launch_rows(RowsArgs &a, int d, bool half, cudaStream_t s)
 {
-    const int rw = 32 / (d / 8);
-    const int groups = (a.q ? (a.H + rw - 1) / rw : 0) + (a.k ? (a.Hk + rw - 1) / rw : 0);
-    const int64_t tokens = (int64_t)a.B * a.L;
-    // Warps per token: one (the angles are formed once) while the tokens alone give every SM
+    const int rw = d == 128 ? ROWS_AT_ONCE<128> : ROWS_AT_ONCE<64>;
+    const int heads_at_once = MANY ? 1 : rw, tokens_at_once = MANY ? rw : 1;
+    const int groups = (a.q ? (a.H + heads_at_once - 1) / heads_at_once : 0) + (a.k ? (a.Hk + heads_at_once - 1) / heads_at_once : 0);
+    const int64_t tokens = (int64_t)a.B * a.L, tiles = (tokens + tokens_at_once - 1) / tokens_at_once;
+    // Warps per tile of tokens: one (the angles are formed once) while the tiles alone give every SM
     // 16 warps, else as many as do, at most one per row group.  (Norm and rotation of 12 + 12
     // heads with 8, 16, 32 and 64 warps an SM: 200 tokens of 8 sequences 8.2, 7.4, 9.4 and
     // 12.3 us; 1560 tokens 7.6, 6.8, 9.3 and 12.5; 4680 tokens 13.6, 13.7, 16.9 and 20.3.)
-    const int64_t want = ((int64_t)device_sms() * 16 + tokens - 1) / tokens;
+    const int64_t want = ((int64_t)device_sms() * 16 + tiles - 1) / tiles;
     a.n_parts = (int32_t)(want < 1 ? 1 : (want > groups ? groups : want));
     if (tokens >= ((int64_t)1 << 31)) return SFA_ERR_INVALID_ARG;  // (parts: only where tokens are few)
-    a.n_warps = (uint32_t)tokens * (uint32_t)a.n_parts;
+    a.tokens = (uint32_t)tokens;
+    a.n_warps = (uint32_t)tiles * (uint32_t)a.n_parts;
     const int64_t grid = ((int64_t)a.n_warps + ROW_WARPS - 1) / ROW_WARPS;
     const dim3 g((unsigned)grid), t(ROW_WARPS * 32);
-    if (d == 128 && half) rows_kernel<128, true, CACHE><<<g, t, 0, s>>>(a);
-    else if (d == 128) rows_kernel<128, false, CACHE><<<g, t, 0, s>>>(a);
-    else if (half) rows_kernel<64, true, CACHE><<<g, t, 0, s>>>(a);
-    else rows_kernel<64, false, CACHE><<<g, t, 0, s>>>(a);
+    if (d == 128 && half) rows_kernel<128, true, CACHE, MANY><<<g, t, 0, s>>>(a);
+    else if (d == 128) rows_kernel<128, false, CACHE, MANY><<<g, t, 0, s>>>(a);
+    else if (half) rows_kernel<64, true, CACHE, MANY><<<g, t, 0, s>>>(a);
+    else rows_kernel<64, false, CACHE, MANY><<<g, t, 0, s>>>(a);
     return launch_status();
+}
+
+// Several tokens a warp: with few heads, whose rows would leave lanes idle and the coefficients
+// unshared, once there are more tokens than warps fit on the GPU.  Norm and rotation of 20000
+// tokens, one and several a warp, H + H_kv = 2, 8, 12, 24: d = 128 19.3, 26.3, 31.2, 47.4 and
+// 13.3, 23.3, 29.4, 49.9 us; d = 64 16.8, 19.4, 23.3, 29.2 and 8.5, 14.4, 18.2, 30.6; 2400 tokens,
+// H + H_kv = 2, 8: 4.7, 5.4 and 4.6, 6.0.  Append at d = 128 24.5, 34.4, 43.0, 70.7 and 16.8, 32.5,
+// 42.8, 74.1.
+template <bool CACHE>
+sfa_status launch_rows(RowsArgs &a, int d, bool half, cudaStream_t s)
+{
+    const int heads = (a.q ? a.H : 0) + (a.k ? a.Hk : 0);
+    const bool many = heads <= 12 && (int64_t)a.B * a.L > (int64_t)device_sms() * ROW_WARPS * ROW_CTAS;
+    return many ? launch_rows<CACHE, true>(a, d, half, s) : launch_rows<CACHE, false>(a, d, half, s);
 }
 
 void fill_cache(RowsArgs &a, const sfa_rows_desc *d, const sfa_cache *cache, const void *k, const void *v,

@@ -43,6 +43,10 @@ NORM_CASES = [
     (1, 16, 8, 9, 64, (0, 48), "half", 1e-6, False, False, "slice"),
     (1, 2, 2, 4099, 128, (2, 0, 4, 8), "interleaved", None, False, True, "bhld"),
     (4, 7, 7, 11, 128, None, "interleaved", 1e-6, True, False, "bhld"),
+    # several tokens a warp
+    (1, 2, 1, 9001, 128, (64,), "half", 1e-6, True, True, "blhd"),
+    (3, 1, 1, 1999, 64, (22, 10), "interleaved", 1e-6, True, False, "slice"),
+    (2, 4, 4, 2600, 128, None, "interleaved", 1e-6, True, False, "bhld"),
 ]
 
 
@@ -301,6 +305,10 @@ APPEND_CASES = [
     # a warp for every token, and more heads than it looks up at a time
     (2, 40, 40, 1250, 64, 16, False, True, "half", (64,)),
     (1, 2, 35, 2400, 128, 24, True, False, "interleaved", (64, 32)),
+    # several tokens a warp
+    (3, 3, 1, 1777, 64, 40, True, True, "half", (32,)),
+    (1, 1, 1, 5001, 128, 16, False, False, "interleaved", (44, 42, 42)),
+    (7, 4, 3, 701, 128, 1560, True, True, "half", (128,)),
 ]
 
 
