@@ -6,7 +6,9 @@
 // heads of a key head sharing its rows.
 //
 // Few query rows (rows_attn_kernel): every code is read once from HBM, converted and used for
-// at most 16 rows, so the floor is the cache's bytes.
+// at most 16 rows, so the floor is the cache's bytes.  Many (tile_attn_kernel): 4 d operations a
+// query and key on the tensor cores.  Where there are few units of work either cuts the keys
+// into ranges, and join_kernel joins their results by the log-sum-exp.
 #include <cuda.h>
 #include <algorithm>
 #include <cmath>
@@ -102,7 +104,7 @@ __device__ __forceinline__ int row_limit(const ChunkArgs &a, const Unit &u, int 
 // longer ranges).
 // With a target, unless the lengths are nearly equal: its share of `target` ranges in all, by the
 // steps of all units, so that all the CTAs start at once and end together (one token, 8 x 12
-// units of 64 to 128 steps: 77 us, against 86 with ranges cut by the bound; at equal lengths 96
+// units of 64 to 128 steps: 76 us, against 86 with ranges cut by the bound; at equal lengths 96
 // against 92, the shares being whole numbers).
 __device__ __forceinline__ int n_ranges(const ChunkArgs &a, int steps, int step_keys)
 {
@@ -205,13 +207,16 @@ __device__ __forceinline__ void skip_range(const ChunkArgs &a, const Unit &u, in
 // ----------------------------------------------------------------- few query rows
 // Sixteen rows against the keys, with the m16n8k16 matrix instruction.  A warp owns every
 // fourth stretch of 32 keys of the CTA's range and streams them through a ring of its own in
-// shared memory, so that the next stretch is on its way while it works on one: with the loads
-// in registers the latency was not covered (130 us against HBM's 50 for one token of 8
-// sequences over 16384 tokens).  The codes are turned into bf16 in the lane layout of the
-// instruction, whose k index may be any order of the elements as long as Q has the same; the
-// key range is cut over warps and CTAs, and the partial results are joined by their log-sum-exp.
-// What bounds it is the conversion: about 2.5 instructions a code, on a pipe that takes one
-// every two cycles, next to 32 matrix instructions of 8 cycles for 16 keys.
+// shared memory, so that the next stretch is on its way while it works on one (one token of 8
+// sequences, 12 heads, 8192 to 16384 tokens, d = 128: 130 us with the loads in registers, 86 with the
+// ring, 76 with ranges cut by the lengths, 4.3 TB/s; HBM's time is 50, the copies alone take 57).
+// The codes are turned into bf16 in the lane layout of the instruction, whose k index may be any
+// order of the elements as long as Q has the same; the key range is cut over warps and CTAs,
+// and the partial results are joined by their log-sum-exp.
+// What bounds it is issue: of some 1000 instructions for 32 keys of 128 elements 64 are matrix
+// instructions and 512 turn codes into bf16, at two warps and a half a scheduler that wait for
+// one another's results (51 % of the issue slots, the integer pipe 46 %).  Sixteen warps an SM instead
+// of twelve, with Q in shared memory to get by on 128 registers: 102 us instead of 86.
 constexpr int FR_WARPS = 4;
 constexpr int FR_ROWS = 16;              // the matrix instruction's rows
 constexpr int FR_STRETCH = 32;           // keys that a warp works on at a time
@@ -686,6 +691,13 @@ __global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
 // (with P in shared memory, as in the frame-list kernel, a key tile took 5600 cycles, 2200 of
 // them in the issue of 11 loads behind blocked stores).  So P stays in tensor memory, in the
 // columns of the S that it comes from or beside it, as the first operand of P V.
+// A unit takes 2.8 us a key tile at d = 128 (900 TFLOP/s; 2.0 us at d = 64), bound by the softmax
+// warps: 256 x 128 exponentials are 2000 cycles of an SM's special-function pipe, and the scores'
+// way out of tensor memory, the maximum, the scaling and the packing are issued beside them.  Its
+// start and end take as long as five key tiles at d = 128 (page lookups, queries, the first
+// conversions; the last product and the rows' way out).  The streaming chunk, 4680 rows of 12
+// heads over 20280 tokens and fewer: 0.389 TFLOP in 552 us, 704 TFLOP/s (with bf16 keys and values
+// in place sfa_forward takes 493).
 // warps 0-3: softmax of query tile A, 4-7: of B
 constexpr int CT_K_WARP = 8;              // 8-11: codes of K to bf16
 constexpr int CT_V_WARP = 12;             // 12-14: of V
@@ -1336,12 +1348,12 @@ constexpr double DEALT_STEPS = 6.0;  // key steps a CTA, below which the lengths
 constexpr int MAX_DEALT = 1024;  // caches (B * H_kv) whose lengths every CTA reads
 
 // Which kernel.  Up to 32 query rows of a key head, 16 rows a CTA read the cache at most twice
-// and win (12 heads x 4 sequences over 8192 tokens, d = 128: 24 rows 56 against 61 us, 32 rows 57
-// against 62, 48 rows 71 against 62; 8 x 8 over 16384, d = 64: 32 rows 77 against 106, 48 rows
-// 107 against 106), and beyond that while all its steps hardly fill the SMs once, where the tile
-// kernel's start and end are most of its time (12 heads over 1560 tokens: 48 rows 13.8 against
-// 16.9, 64 rows 16.4 against 17.0, 96 rows 19.5 against 17.3; 4 heads over 300 tokens, d = 64:
-// 128 rows 7.3 against 11.5).
+// and win (12 heads x 4 sequences over 8192 tokens, d = 128: 24 rows 47 against 54 us, 32 rows 47
+// against 54, 48 rows 64 against 54; 8 x 8 over 16384, d = 64: 32 rows 73 against 104, 48 rows
+// 104 against 104), and beyond that while all its steps hardly fill the SMs once, where the tile
+// kernel's start and end are most of its time (12 heads over 1560 tokens: 48 rows 13.7 against
+// 14.8, 64 rows 15.7 against 14.9, 96 rows 18.3 against 15.3; 4 heads over 300 tokens, d = 64:
+// 128 rows 7.5 against 10.7).
 bool few_rows(const sfa_cache_attn_desc *d, int64_t rows, int64_t kv)
 {
     if (d->debug_flags & SFA_DEBUG_CACHE_TILES) return false;
@@ -1366,8 +1378,8 @@ Plan plan_of(const sfa_cache_attn_desc *d, const sfa_cache *c)
     // the device, so the mean of two cases is taken: all caches as long as the bound (whole
     // waves of equal ranges), and lengths spread between half of it and all of it (three
     // quarters of the ranges, which then even out but for the last one's end).  Measured, one
-    // token, 96 units of 128 steps, k = 3, 6, 9, 12, 18: 103, 106, 100, 105, 107 us at one
-    // length and 98, 107, 85, 91, 88 at uneven ones; 32 units: k = 9, 13, 18: 43, 41, 49.
+    // token, 96 units of 128 steps, k = 3, 6, 9, 12, 18: 99, 111, 92, 101, 101 us at one
+    // length and 94, 100, 86, 87, 82 at uneven ones; 32 units, k = 9, 13, 18: 42, 37, 46 and 40, 37, 34.
     const double slots = (double)attn_sms() * (p.tiles ? 1 : FR_CTAS);
     const double fixed = p.tiles ? 5.0 : 2.0;
     double best = 1e300;
