@@ -1,10 +1,12 @@
-"""Build libsfa.so in-tree with nvcc for sm_100a (B200).
+"""Build libsfa.so in-tree with nvcc for sm_100a (B200), and the extension module _bind.so.
 
     python -m frame_sparse_attention_b200.build [--force] [--verbose-ptxas]
 
 Each csrc/*.cu is compiled to an object under _build/ (rebuilt when it or a header
 changed), then linked into frame_sparse_attention_b200/libsfa.so with the CUDA
-runtime linked statically.  No GPU is needed to build.
+runtime linked statically; csrc/sfa_bind.cpp, the binding of the 8-bit frame cache's calls,
+is built with the C++ compiler against PyTorch's headers and libsfa.so.  No GPU is needed to
+build.
 """
 from __future__ import annotations
 
@@ -13,6 +15,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsfa.so")
+BIND = os.path.join(PKG, "_bind.so")
+BIND_SRC = os.path.join(CSRC, "sfa_bind.cpp")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -35,6 +40,24 @@ def _newest_header() -> float:
     hdrs = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
     hdrs += glob.glob(os.path.join(INCLUDE, "*.h"))
     return max((os.path.getmtime(h) for h in hdrs), default=0.0)
+
+
+def _build_bind(nvcc: str, force: bool) -> None:
+    """_bind.so, with torch's own libraries as they are loaded already by `import torch`."""
+    newest = max(os.path.getmtime(BIND_SRC), _newest_header())
+    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= newest:
+        return
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    inc = [INCLUDE, *include_paths(), cuda, sysconfig.get_paths()["include"]]
+    tmp = BIND + f".tmp{os.getpid()}"
+    subprocess.check_call([shutil.which("g++") or "c++", "-std=c++17", "-O2", "-fPIC", "-shared",
+                           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                           *(f"-isystem{i}" for i in inc), BIND_SRC, "-o", tmp,
+                           *(f"-L{i}" for i in library_paths()), f"-L{PKG}", "-l:libsfa.so", "-Wl,-rpath,$ORIGIN",
+                           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
+    os.replace(tmp, BIND)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -60,6 +83,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         subprocess.check_call([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    _build_bind(nvcc, force)
     return LIB
 
 

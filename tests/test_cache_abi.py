@@ -292,3 +292,32 @@ def test_attention_binding_refuses_wrong_tensors(sfa):
         a.update(over)
         with pytest.raises((ValueError, sfa.SfaError)):
             sfa.forward_cache(**a)
+
+
+def test_binding_refuses_what_is_no_tensor_or_no_number(sfa):
+    q = torch.zeros(2, 4, 8, 64, dtype=torch.bfloat16)
+    cache = sfa.cache_create(4, 16, 64, heads=2, device="cpu")
+    table, lens = torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    good = dict(q=q, cache=cache, table=table, kv_lens=lens)
+    for over, error in ((dict(q=None), TypeError), (dict(table=[0]), TypeError), (dict(kv_lens=3), TypeError),
+                        (dict(cache=cache[:3]), ValueError), (dict(cache=5), TypeError), (dict(max_kv=1 << 40), ValueError),
+                        (dict(max_kv="8"), TypeError), (dict(timeout_us=-1), ValueError), (dict(debug_flags=1 << 32), ValueError),
+                        (dict(scale="1"), TypeError), (dict(H_kv=1 << 35), ValueError), (dict(lse=0), TypeError),
+                        (dict(stream=7), ValueError), (dict(kv_lens=torch.tensor(1, dtype=torch.int32)), ValueError),
+                        (dict(table=torch.tensor(1, dtype=torch.int32)), ValueError), (dict(q=q[0]), ValueError)):
+        with pytest.raises(error):
+            sfa.forward_cache(**{**good, **over})
+    rope = sfa.rope_table((64,), device="cpu")
+    pos = torch.zeros(8, 1, dtype=torch.int32)
+    for over, error in ((dict(rope=rope[:2]), ValueError), (dict(rope=3), TypeError), (dict(layout=None), ValueError),
+                        (dict(rope=rope._replace(axis_pairs=())), ValueError), (dict(eps="1"), TypeError),
+                        (dict(rope=rope._replace(axis_pairs=(8,) * 5)), ValueError), (dict(positions=3), TypeError),
+                        (dict(q_weight=1.0), TypeError), (dict(q_out=1), TypeError)):
+        with pytest.raises(error):
+            sfa.qk_norm_rope(q, **{**dict(rope=rope, positions=pos), **over})
+    with pytest.raises(ValueError):
+        sfa.qk_norm_rope(None, None)
+    for over, error in ((dict(L=-1), ValueError), (dict(L=1 << 31), ValueError), (dict(L=None), TypeError),
+                        (dict(H_kv=0), ValueError), (dict(table=torch.tensor(1, dtype=torch.int32)), ValueError)):
+        with pytest.raises(error):
+            sfa.cache_read(**{**dict(cache=cache, table=table, start=lens, L=8), **over})

@@ -425,3 +425,28 @@ def test_a_query_with_nan_answers_nan(L, kv, flags):
     rest = [i for i in range(L) if i != 1]
     k, v = gather(cache, table, 0, 0, kv)
     check(o[0, 0, rest], l[0, 0, rest], f64(q[0, 0, rest]), k, v, 0.125, False)
+
+
+def test_calls_of_two_threads():
+    """Each thread has a stream and outputs of its own; the cache is read by both."""
+    from concurrent.futures import ThreadPoolExecutor
+    m, g = sfa(), np.random.default_rng(11)
+    cache = random_pool(g, m, 40, 2, 64, 64)
+    table = torch.arange(40, dtype=torch.int32, device="cuda").reshape(1, 40)
+    lens = torch.tensor([2500], dtype=torch.int32, device="cuda")
+    start = torch.zeros(1, dtype=torch.int32, device="cuda")
+    qs = [torch.from_numpy(g.standard_normal((1, 4, n, 64))).bfloat16().cuda() for n in (1, 200)]
+    want = [(m.forward_cache(q, cache, table, lens), m.cache_read(cache, table, start, 300)) for q in qs]
+    torch.cuda.synchronize()
+
+    def work(q):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            r = [(m.forward_cache(q, cache, table, lens), m.cache_read(cache, table, start, 300)) for _ in range(50)]
+        stream.synchronize()
+        return r
+    with ThreadPoolExecutor(2) as ex:
+        for w, got in zip(want, ex.map(work, qs)):
+            for r in got:
+                for a, b in zip(w, r):
+                    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
