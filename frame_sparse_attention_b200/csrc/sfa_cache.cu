@@ -72,16 +72,19 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 
 // cosine and sine (times the scale) of pair p at this token.  A far position times a
 // frequency loses its fraction of a turn in fp32, so the product is formed and reduced to
-// [-1, 1] half turns in fp64; what is left is exact to fp32.
+// [-1, 1] half turns in fp64.  What fp32 drops of that (up to 2^-25 half turns, 9e-8 of a radian,
+// more than the rounding of the results) turns the pair by a first-order step.
 __device__ __forceinline__ float2 rotation(const RowsArgs &a, const int32_t *pos, int p)
 {
     int ax = 0;
 #pragma unroll
     for (int i = 0; i < SFA_ROPE_MAX_AXES - 1; ++i) ax += (i < a.n_axes - 1 && p >= a.axis_end[i]) ? 1 : 0;
     const double t = (double)__ldg(pos + ax) * __ldg(a.inv_freq + p) * 0.31830988618379067154;
+    const double r = t - 2.0 * rint(0.5 * t);
+    const float near = (float)r, rest = (float)(r - near) * 3.14159265358979f;
     float s, c;
-    sincospif((float)(t - 2.0 * rint(0.5 * t)), &s, &c);
-    return make_float2(c * a.rope_scale, s * a.rope_scale);
+    sincospif(near, &s, &c);
+    return make_float2(fmaf(-rest, s, c) * a.rope_scale, fmaf(rest, c, s) * a.rope_scale);
 }
 
 // Two fp32 numbers that one instruction works on (each rounds like a scalar).
