@@ -151,7 +151,8 @@ def cache_read(cache: FrameCache, table, start, L: int, lens=None, k_out=None, v
 
 
 def forward_cache_workspace_bytes(q, cache: FrameCache, table, kv_lens, max_kv: int = 0, H_kv: int | None = None) -> int:
-    """Device workspace bytes of forward_cache for these shapes."""
+    """Device workspace bytes of forward_cache for these shapes (kv_lens as in the call: one length for
+    all heads or one each)."""
     return (_bind or _load_bind()).forward_cache_workspace(q, cache, table, kv_lens, max_kv, H_kv)
 
 

@@ -476,6 +476,7 @@ PyObject *forward_cache_workspace(PyObject *, PyObject *const *x, Py_ssize_t n)
     desc.d = size32(s[3]);
     desc.scale = 1.f;
     desc.max_kv = integer<int32_t>("max_kv", x[4]);
+    per_head("kv_lens", x[3], dev, s[0], H_kv, desc.len_stride);
     size_t bytes = 0;
     check(sfa_forward_cache_workspace(&desc, &cache, &bytes), "sfa_forward_cache_workspace");
     return PyLong_FromSize_t(bytes);

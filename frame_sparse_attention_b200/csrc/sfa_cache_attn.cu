@@ -38,8 +38,9 @@ struct ChunkArgs {
     float *lse;
     int32_t *status;
     int32_t n_row_tiles, n_split;
-    int32_t range_len;  // key steps of a range, see n_ranges
-    int32_t target;     // > 0: CTAs that the lengths on the device are dealt out to
+    int32_t range_len;  // key steps of a range, see Unit::len
+    int32_t target;     // > 0: CTAs that the ranges are dealt out to by the lengths on the device
+    int32_t even_split; // ranges of a cache, at most, without a target or where all are about as long
     float *part_o;    // [n_split][B * H * Lq][d], normalised, when n_split > 1
     float *part_lse;  // [n_split][B * H * Lq], log2 units
     uint64_t timeout_ns;
@@ -60,27 +61,125 @@ constexpr float EQUAL_LENGTHS = 0.93f;  // mean over longest, from which the cac
 // head hk * G + r % G, and its share of the keys those rows see.
 struct Unit {
     int b, hk, row0, split;
+    int ranges;   // that the unit's keys are cut into, at most
+    int len;      // key steps of a range, at least
     int m, n;     // query tokens and cache tokens
     int n_rows;   // m * G
     bool bad;     // n outside the table
 };
 
-__device__ __forceinline__ Unit open_unit(const ChunkArgs &a, int tile_rows)
+constexpr int MAX_DEALT = 128;  // caches (B * H_kv) whose lengths a warp goes through
+
+// Key steps of the i-th cache, cut at 2^20: so that MAX_DEALT of them add up in 32 bits, and for
+// exact quotients in fp32 below (t + len - 1/2 has 22 bits, and no multiple of len within 1/2).
+__device__ __forceinline__ int steps_of(const ChunkArgs &a, int i, int step_keys)
+{
+    if (i >= a.B * a.Hk) return 0;
+    const int b = (int)(((float)i + 0.5f) * (1.f / (float)a.Hk));
+    const int n = __ldg(a.kv_lens + b * a.ls0 + (i - b * a.Hk) * a.ls1);
+    return n > 0 && n <= a.cache.table_len * a.cache.page_len ? min((n + step_keys - 1) / step_keys, 1 << 20) : 0;
+}
+
+// CTA x's cache, row tile and range where the caches' lengths differ (every lane of a warp calls it;
+// false: there is none).  Ranges have the shortest length that makes no more than `target` of them,
+// so that all start at once and end about together, and the CTAs with a range are the first
+// ones: where CTAs without one lay between, a launch of 64 two-tile units took 51 us for 37, each
+// holding its SM for a few us.  The loops are short code, which runs once.
+// Against ranges cut by the bound alone, us: one token, 8 x 12 caches of 16384 at most, d = 128: half to
+// all of it 86, now 74, one long and the rest a quarter 49 (shares by length) and 41; 12 caches of 6,
+// 7 or 13 frames under 200 and 1000 rows 53 and 159, now 45 and 132; 2 x 333 causal rows, 12 on 4
+// heads, d = 64, over 4099 and less 34.8, now 30.8; 32 caches of 8192, d = 128, 100 rows, one long
+// 40.4, now 29.  Where all are equal the tile kernel pays for looking: 34.9 and 36.9, 55.4 and
+// 57.4, 42.9 and 47.2, one token 95.7 and 96.6.
+__device__ __forceinline__ bool deal(const ChunkArgs &a, int step_keys, int total, int longest, int x, int &cache,
+                                     int &tile, Unit &u)
+{
+    const int heads = a.B * a.Hk, lane = threadIdx.x & 31;
+    const int room = a.target / a.n_row_tiles;  // ranges of one row tile of all caches; `heads` or more
+    float per_len;
+    int len = max(1, (total + room - 1) / room);
+    auto ranges_of = [&](int i) {
+        const int r = (int)(((float)(steps_of(a, i, step_keys) + len) - 0.5f) * per_len);
+        return i < heads ? max(1, r) : 0;
+    };
+#pragma unroll 1
+    for (;; len += 1 + (len >> 4)) {
+        per_len = 1.f / (float)len;
+        int count = 0;
+#pragma unroll 1
+        for (int i = lane; i < heads; i += 32) count += ranges_of(i);
+        if (len >= longest || __reduce_add_sync(0xffffffffu, count) <= room) break;
+    }
+#pragma unroll 1
+    for (int i0 = 0; i0 < heads; i0 += 32) {
+        const int mine = min(a.n_split, ranges_of(i0 + lane));
+        int upto = mine * a.n_row_tiles;  // CTAs of the caches up to this lane's
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, o);
+            upto += lane >= o ? y : 0;
+        }
+        const int all = __shfl_sync(0xffffffffu, upto, 31);
+        if (x < all) {
+            const int at = __ffs(__ballot_sync(0xffffffffu, x < upto)) - 1;
+            u.ranges = __shfl_sync(0xffffffffu, mine, at);
+            x -= __shfl_sync(0xffffffffu, upto, at) - u.ranges * a.n_row_tiles;
+            cache = i0 + at;
+            tile = x / u.ranges;
+            u.split = x - tile * u.ranges;
+            u.len = 1;
+            return true;
+        }
+        x -= all;
+    }
+    return false;
+}
+
+// DEAL: the launch may have a target.  (A kernel of its own with many rows: the code above, only
+// jumped over, cost the streaming chunk 571 us instead of 555.)
+template <bool DEAL>
+__device__ __forceinline__ Unit open_unit(const ChunkArgs &a, int tile_rows, int step_keys)
 {
     Unit u;
-    int x = blockIdx.x;
-    if (a.target) {  // the CTAs that may have no range of their own come last
-        const int units = gridDim.x / a.n_split;
-        u.split = x / units;
-        x -= u.split * units;
-    } else {
-        u.split = x % a.n_split;
-        x /= a.n_split;
+    int x = blockIdx.x, rt = 0;
+    bool even = true, there = true;
+    u.ranges = a.even_split;
+    u.len = a.range_len;
+    if (DEAL && a.target) {
+        const int heads = a.B * a.Hk;
+        int total = 0, longest = 0;
+#pragma unroll 1
+        for (int i = threadIdx.x & 31; i < heads; i += 32) {
+            const int t = steps_of(a, i, step_keys);
+            total += t;
+            longest = max(longest, t);
+        }
+        total = __reduce_add_sync(0xffffffffu, total);
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        even = (float)total >= EQUAL_LENGTHS * longest * heads;
+        if (!even) there = deal(a, step_keys, total, longest, x, x, rt, u);
+    }
+    if (even) {  // the host's plan for the bound, which may take several waves
+        u.split = x % a.even_split;
+        x /= a.even_split;
+        rt = x % a.n_row_tiles;
+        x /= a.n_row_tiles;
+        there = x < a.B * a.Hk;
+    }
+    if (DEAL) {  // (in uniform registers again, as what comes of the block's number alone is)
+        x = __reduce_max_sync(0xffffffffu, there ? x : -1);
+        rt = __reduce_max_sync(0xffffffffu, rt);
+        u.split = __reduce_max_sync(0xffffffffu, u.split);
+        u.ranges = __reduce_max_sync(0xffffffffu, u.ranges);
+        u.len = __reduce_max_sync(0xffffffffu, u.len);
+    }
+    if (DEAL && x < 0) {
+        u.bad = false;
+        u.row0 = u.n_rows = 0;
+        return u;
     }
     // causal: the last row tiles see the most keys and start first
-    const int rt = x % a.n_row_tiles;
     u.row0 = (a.causal ? a.n_row_tiles - 1 - rt : rt) * tile_rows;
-    x /= a.n_row_tiles;
     u.hk = x % a.Hk;
     u.b = x / a.Hk;
     u.m = a.q_lens ? min(max(__ldg(a.q_lens + u.b), 0), a.Lq) : a.Lq;
@@ -98,34 +197,12 @@ __device__ __forceinline__ int row_limit(const ChunkArgs &a, const Unit &u, int 
     return a.causal ? max(0, min(u.n, u.n - u.m + r / a.G + 1)) : u.n;
 }
 
-// Ranges that the key steps of a unit are cut into (every lane of a warp calls it): as many of
-// range_len steps as it has, so that long and short caches give pieces of one length, but never
-// more than the n_split CTAs that it was given (caches longer than the caller's bound just get
-// longer ranges).
-// With a target, unless the lengths are nearly equal: its share of `target` ranges in all, by the
-// steps of all units, so that all the CTAs start at once and end together (one token, 8 x 12
-// units of 64 to 128 steps: 76 us, against 86 with ranges cut by the bound; at equal lengths 96
-// against 92, the shares being whole numbers).
-__device__ __forceinline__ int n_ranges(const ChunkArgs &a, int steps, int step_keys)
+// Ranges that the key steps of a unit are cut into: as many of `len` steps as it has, so that long
+// and short caches give pieces of one length, but never more than the CTAs that it was given
+// (caches longer than the caller's bound just get longer ranges).
+__device__ __forceinline__ int n_ranges(const Unit &u, int steps)
 {
-    if (a.target) {
-        const int heads = a.B * a.Hk;
-        int total = 0, longest = 0;
-        for (int x = threadIdx.x & 31; x < heads; x += 32) {
-            const int b = x / a.Hk, n = __ldg(a.kv_lens + b * a.ls0 + (x - b * a.Hk) * a.ls1);
-            // (cut at 2^20 so that 1024 of them add up in 32 bits)
-            const int t = n > 0 && n <= a.cache.table_len * a.cache.page_len ? min((n + step_keys - 1) / step_keys, 1 << 20) : 0;
-            total += t;
-            longest = max(longest, t);
-        }
-        const float sum = (float)__reduce_add_sync(0xffffffffu, total);
-        longest = __reduce_max_sync(0xffffffffu, longest);
-        if (sum < EQUAL_LENGTHS * longest * heads) {
-            const int share = (int)(steps * (a.target / (fmaxf(sum, 1.f) * a.n_row_tiles)) + 0.5f);
-            return max(1, min(min(a.n_split, steps), share));
-        }
-    }
-    return max(1, min(a.n_split, (steps + a.range_len - 1) / a.range_len));
+    return max(1, min(u.ranges, (steps + u.len - 1) / u.len));
 }
 
 // Row `id` of the outputs: (b * H + h) * Lq + i for row r of a unit.
@@ -196,12 +273,24 @@ struct RowOut {
     }
 };
 
-// A CTA without a range of its own leaves "nothing seen" for its rows.
-__device__ __forceinline__ void skip_range(const ChunkArgs &a, const Unit &u, int tile_rows)
+// The log-sum-exp of a row in this CTA's range, and "nothing seen" in the ranges that no CTA has:
+// every `ranges`-th from its own on.
+template <bool DEAL>
+__device__ __forceinline__ void put_part_lse(const ChunkArgs &a, int split, int ranges, int64_t id, float lse2)
 {
     const int64_t part_rows = (int64_t)a.B * a.H * a.Lq;
+    a.part_lse[split * part_rows + id] = lse2;
+    if (!DEAL) return;
+#pragma unroll 1
+    for (int s = split + ranges; s < a.n_split; s += ranges) a.part_lse[s * part_rows + id] = -INFINITY;
+}
+
+// A CTA whose rows see too few keys for its range leaves "nothing seen".
+template <bool DEAL>
+__device__ __forceinline__ void skip_range(const ChunkArgs &a, const Unit &u, int tile_rows)
+{
     for (int r = u.row0 + threadIdx.x; r < min(u.row0 + tile_rows, u.n_rows); r += blockDim.x)
-        a.part_lse[(int64_t)u.split * part_rows + row_id(a, u, r)] = -INFINITY;
+        put_part_lse<DEAL>(a, u.split, u.ranges, row_id(a, u, r), -INFINITY);
 }
 
 // ----------------------------------------------------------------- few query rows
@@ -209,7 +298,7 @@ __device__ __forceinline__ void skip_range(const ChunkArgs &a, const Unit &u, in
 // fourth stretch of 32 keys of the CTA's range and streams them through a ring of its own in
 // shared memory, so that the next stretch is on its way while it works on one (one token of 8
 // sequences, 12 heads, 8192 to 16384 tokens, d = 128: 130 us with the loads in registers, 86 with the
-// ring, 76 with ranges cut by the lengths, 4.3 TB/s; HBM's time is 50, the copies alone take 57).
+// ring, 74 to 76 with ranges cut by the lengths, 4.3 TB/s; HBM's time is 50, the copies alone take 57).
 // The codes are turned into bf16 in the lane layout of the instruction, whose k index may be any
 // order of the elements as long as Q has the same; the key range is cut over warps and CTAs,
 // and the partial results are joined by their log-sum-exp.
@@ -326,14 +415,14 @@ __global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     if (a.n_split > 1) pdl_launch_dependents();  // the joining kernel's CTAs may take their places
-    const Unit u = open_unit(a, FR_ROWS);
+    const Unit u = open_unit<true>(a, FR_ROWS, FR_KEYS);
     if (u.bad && tid == 0) report_status(a.status, SFA_ERR_BAD_SET);
     if (u.row0 >= u.n_rows) return;  // rows behind this sequence's last
     // the tile's last row sees the most keys
     const int seen = row_limit(a, u, min(u.row0 + FR_ROWS, u.n_rows) - 1);
     const int steps = (seen + FR_KEYS - 1) / FR_KEYS;
-    const int ranges = n_ranges(a, steps, FR_KEYS);
-    if (u.split >= ranges) return skip_range(a, u, FR_ROWS);
+    const int ranges = n_ranges(u, steps);
+    if (u.split >= ranges) return skip_range<true>(a, u, FR_ROWS);
     const int s0 = (int)((int64_t)steps * u.split / ranges), s1 = (int)((int64_t)steps * (u.split + 1) / ranges);
     // this warp's stretches: keys FR_KEYS (s0 + k) + 32 warp .. + 31, those that start before the end
     const int key0 = s0 * FR_KEYS + warp * FR_STRETCH;
@@ -344,7 +433,11 @@ __global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
     const uint32_t bars = sbase + C::SMEM_BARS + warp * FR_STAGES * 8;
     volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(smem + C::SMEM_FLAGS);
     if (lane < FR_STAGES) mbar_init(bars + 8 * lane, BULK ? 1 : 32);
-    if (tid == 0) *abort_flag = 0;
+    volatile int32_t *ranges_sh = abort_flag + 1;  // (not in a register until the end)
+    if (tid == 0) {
+        *abort_flag = 0;
+        *ranges_sh = u.ranges;
+    }
     fence_mbar_init();
     __syncthreads();
     const Ctl ctl{abort_flag, a.status, a.timeout_ns};
@@ -670,7 +763,7 @@ __global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
             float4 *dst = reinterpret_cast<float4 *>(a.part_o + ((int64_t)u.split * part_rows + id) * D + e0);
             dst[0] = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
             dst[1] = make_float4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv);
-            if (e0 == 0) a.part_lse[(int64_t)u.split * part_rows + id] = lse2;
+            if (e0 == 0) put_part_lse<true>(a, u.split, *ranges_sh, id, lse2);
         }
     }
 }
@@ -1055,7 +1148,7 @@ __device__ __forceinline__ bool chunk_softmax_tile(uint32_t t_s, uint32_t t_p, u
 }
 
 // Queries, softmax and epilogue of query tile x, one thread per row.
-template <int D>
+template <int D, bool DEAL>
 __device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *smem, uint32_t sbase,
                                    const volatile uint32_t *tmem_slot, const volatile int32_t *skip, int x, int key0,
                                    int n_tiles, bool one_tile, const Ctl &ctl)
@@ -1065,6 +1158,7 @@ __device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *s
     constexpr int RPI = 32 / LR;  // rows per access of a warp
     const CBars<D> bar{sbase + C::SMEM_BAR};
     volatile int32_t *epi_ok = reinterpret_cast<volatile int32_t *>(smem + C::SMEM_BAR + 160) + 4 * x;
+    const volatile int32_t *ranges_sh = reinterpret_cast<const volatile int32_t *>(smem + C::SMEM_BAR + 252);
     const int row = threadIdx.x & 127, lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
     const int tile_row0 = u.row0 + x * BM;
     const uint32_t s_tile = sbase + C::SMEM_Q + x * C::TILE_BYTES;
@@ -1163,7 +1257,7 @@ __device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *s
         }
     }
     if (there) {
-        if (a.n_split > 1) a.part_lse[u.split * part_rows + row_id(a, u, r)] = lse2;
+        if (a.n_split > 1) put_part_lse<DEAL>(a, u.split, DEAL ? *ranges_sh : 0, row_id(a, u, r), lse2);
         else a.lse[row_id(a, u, r)] = lse2 * 0.69314718055994530942f;
     }
     __syncwarp();  // a warp stores the 32 rows that its lanes have staged, whole rows at a time
@@ -1186,7 +1280,7 @@ __device__ void chunk_softmax_role(const ChunkArgs &a, const Unit &u, uint8_t *s
     });
 }
 
-template <int D>
+template <int D, bool DEAL>
 __global__ void __launch_bounds__(CT_THREADS, 1) tile_attn_kernel(const __grid_constant__ ChunkArgs a)
 {
     using C = CCfg<D>;
@@ -1198,13 +1292,13 @@ __global__ void __launch_bounds__(CT_THREADS, 1) tile_attn_kernel(const __grid_c
     volatile int32_t *skip = reinterpret_cast<volatile int32_t *>(smem + C::SMEM_BAR + 248);
     const int warp = threadIdx.x >> 5;
     if (a.n_split > 1) pdl_launch_dependents();
-    const Unit u = open_unit(a, CT_ROWS);
+    const Unit u = open_unit<DEAL>(a, CT_ROWS, BN);
     if (u.bad && threadIdx.x == 0) report_status(a.status, SFA_ERR_BAD_SET);
     if (u.row0 >= u.n_rows) return;
     const int seen = row_limit(a, u, min(u.row0 + CT_ROWS, u.n_rows) - 1);
     const int all = (seen + BN - 1) / BN;
-    const int ranges = n_ranges(a, all, BN);
-    if (u.split >= ranges) return skip_range(a, u, CT_ROWS);
+    const int ranges = n_ranges(u, all);
+    if (u.split >= ranges) return skip_range<DEAL>(a, u, CT_ROWS);
     const int t0 = (int)((int64_t)all * u.split / ranges);
     const int n_tiles = (int)((int64_t)all * (u.split + 1) / ranges) - t0;
     const bool has_b = u.row0 + BM < u.n_rows;
@@ -1217,6 +1311,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1) tile_attn_kernel(const __grid_c
         mbar_init(bar.p_full(0), BM / 32);
         mbar_init(bar.p_full(1), BM / 32);
         *abort_flag = 0;
+        if (DEAL) *reinterpret_cast<volatile int32_t *>(smem + C::SMEM_BAR + 252) = u.ranges;  // (not in a register until the end)
         // once a CTA has timed out, the ones that start later skip their work
         *skip = (a.status && *reinterpret_cast<volatile int32_t *>(a.status) == SFA_ERR_TIMEOUT) ? 1 : 0;
         fence_mbar_init();
@@ -1238,7 +1333,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1) tile_attn_kernel(const __grid_c
     } else if (warp >= CT_K_WARP) {
         convert_role<D, true>(a, u, sbase, t0 * BN, seen, n_tiles, skip, ctl);
     } else if (warp < 4 || has_b) {
-        chunk_softmax_role<D>(a, u, smem, sbase, tmem_slot, skip, warp >> 2, t0 * BN, n_tiles, !has_b, ctl);
+        chunk_softmax_role<D, DEAL>(a, u, smem, sbase, tmem_slot, skip, warp >> 2, t0 * BN, n_tiles, !has_b, ctl);
     } else {
         block_meets();
     }
@@ -1285,12 +1380,15 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
 #pragma unroll
     for (int j = 0; j < E; ++j) acc[j] = 0.f;
     const float *src = a.part_o + id * D + lane * E;
-    for (int s0 = 0; s0 < a.n_split; s0 += 8) {
+    // (ranges behind the last that has anything are not gone through)
+    const uint32_t on0 = __ballot_sync(0xffffffffu, w0 != 0.f), on1 = __ballot_sync(0xffffffffu, w1 != 0.f);
+    const int last = on1 ? 64 - __clz(on1) : 32 - __clz(on0);
+    for (int s0 = 0; s0 < last; s0 += 8) {
         float x[8][E], w[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int s = s0 + k;
-            w[k] = s < a.n_split ? __shfl_sync(0xffffffffu, s0 < 32 ? w0 : w1, s & 31) : 0.f;
+            w[k] = s < last ? __shfl_sync(0xffffffffu, s0 < 32 ? w0 : w1, s & 31) : 0.f;
 #pragma unroll
             for (int j = 0; j < E; ++j) x[k][j] = 0.f;
             if (w[k] != 0.f) {  // (the partial O of a range with weight 0 need not be there)
@@ -1339,13 +1437,12 @@ sfa_status check_attn(const sfa_cache_attn_desc *d)
 
 struct Plan {
     bool tiles;  // tile_attn_kernel, else rows_attn_kernel
-    int row_tiles, n_split, range_len, target;
+    int row_tiles, n_split, range_len, target, even_split;
     int64_t ctas;
 };
 
 constexpr int FEW_ROWS = 32;
 constexpr double DEALT_STEPS = 6.0;  // key steps a CTA, below which the lengths are not dealt out
-constexpr int MAX_DEALT = 1024;  // caches (B * H_kv) whose lengths every CTA reads
 
 // Which kernel.  Up to 32 query rows of a key head, 16 rows a CTA read the cache at most twice
 // and win (12 heads x 4 sequences over 8192 tokens, d = 128: 24 rows 47 against 54 us, 32 rows 47
@@ -1395,29 +1492,43 @@ Plan plan_of(const sfa_cache_attn_desc *d, const sfa_cache *c)
         }
     }
     p.range_len = (int)std::min<int64_t>((steps + p.n_split - 1) / p.n_split, 1 << 30);
-    // Few rows: uneven caches are better cut by their own lengths, into as many ranges as start
-    // at once less a few for the rounding (n_ranges), while that leaves a unit some four ranges
-    // and a range six steps at lengths of three quarters of the bound (five waves and 8 steps,
-    // 32 x 8 caches of 8192: 104 us cut by the bound, 116 by the lengths; one wave and 5 steps,
-    // 4 x 12 of 8192, d = 64: 21.2 and 23.3).  Twice the mean number of CTAs a unit: lengths up
-    // to twice the mean have ranges like the others.
+    // Uneven caches are better cut by their own lengths, into as many ranges as start at once
+    // (`deal`), while that leaves a unit several ranges (64 units, many rows: 36.9 us by the bound
+    // and 39.0 by the lengths) and a range enough steps (few rows, cut by
+    // the bound and by the lengths: five waves and 8 steps, 32 x 8 caches of 8192, 104 and 116 us; one
+    // wave and 5 steps, 4 x 12 of 8192, d = 64, 21.2 and 23.3).  n_split, the ranges that there is
+    // room for, is then twice the mean number of a unit, so that lengths up to twice the mean have
+    // ranges like the others; with many rows, whose partial results are larger, 1.5 times (twice:
+    // 59.4 for 57.4 us at 12 equal caches of 20280, 200 rows).
     p.target = 0;
-    if (!p.tiles && 4.0 * units <= slots && (int64_t)d->B * d->H_kv <= MAX_DEALT && 0.75 * units * steps >= DEALT_STEPS * slots) {
-        p.target = (int)(0.96 * slots);
-        p.n_split = (int)std::min<int64_t>(std::min<int64_t>(MAX_SPLIT, steps), 2 * ((p.target + units - 1) / units));
-    }
+    p.even_split = p.n_split;
     p.ctas = units * p.n_split;
+    const bool lengths = d->B > 1 || (d->H_kv > 1 && d->len_stride[1] != 0);  // more than one
+    const bool dealt = lengths && (p.tiles ? p.n_split > 1 && 3.0 * units <= slots
+                                           : 4.0 * units <= slots && 0.75 * units * steps >= DEALT_STEPS * slots);
+    if (dealt && (int64_t)d->B * d->H_kv <= MAX_DEALT) {
+        p.target = (int)slots;
+        const int64_t mean = (p.target + units - 1) / units, room = p.tiles ? (3 * mean + 1) / 2 : 2 * mean;
+        p.n_split = (int)std::max<int64_t>(std::min<int64_t>(std::min<int64_t>(MAX_SPLIT, steps), room), p.even_split);
+        p.ctas = std::max<int64_t>(p.target, units * p.even_split);
+    }
     return p;
+}
+
+template <int D, bool DEAL>
+sfa_status launch_tiles(const ChunkArgs &a, unsigned grid, cudaStream_t s)
+{
+    if (cudaFuncSetAttribute(tile_attn_kernel<D, DEAL>, cudaFuncAttributeMaxDynamicSharedMemorySize, CCfg<D>::SMEM_BYTES) !=
+        cudaSuccess)
+        return SFA_ERR_CUDA;
+    tile_attn_kernel<D, DEAL><<<grid, CT_THREADS, CCfg<D>::SMEM_BYTES, s>>>(a);
+    return launch_status();
 }
 
 template <int D>
 sfa_status launch_tiles(const ChunkArgs &a, unsigned grid, cudaStream_t s)
 {
-    if (cudaFuncSetAttribute(tile_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, CCfg<D>::SMEM_BYTES) !=
-        cudaSuccess)
-        return SFA_ERR_CUDA;
-    tile_attn_kernel<D><<<grid, CT_THREADS, CCfg<D>::SMEM_BYTES, s>>>(a);
-    return launch_status();
+    return a.target ? launch_tiles<D, true>(a, grid, s) : launch_tiles<D, false>(a, grid, s);
 }
 
 typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
@@ -1531,6 +1642,7 @@ extern "C" sfa_status sfa_forward_cache(const sfa_cache_attn_desc *d, const sfa_
     a.part_lse = a.part_o ? a.part_o + (int64_t)p.n_split * rows * d->d : nullptr;
     a.range_len = p.range_len;
     a.target = p.target;
+    a.even_split = p.even_split;
     a.timeout_ns = (uint64_t)(d->timeout_us ? d->timeout_us : DEFAULT_TIMEOUT_US) * 1000;
     a.debug_flags = d->debug_flags;
     cudaStream_t s = as_cuda(stream);

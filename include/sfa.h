@@ -582,6 +582,7 @@ sfa_status sfa_cache_read(const sfa_rows_desc *desc, const sfa_cache *cache, con
  *   q, o      bf16 [B][H][Lq][d], strides in the descriptor; head h reads key head h / (H / H_kv).
  *   kv_lens   device int32, n = kv_lens[b * len_stride[0] + hk * len_stride[1]]: the keys and
  *             values are logical tokens [0, n) of (b, hk).  n = 0 gives O = 0, LSE = -inf.
+ *             (B = 1 with len_stride[1] = 0, one length for all, spares the look at the others.)
  *   q_lens    device int32 [B] or NULL (= Lq): only rows i < m = q_lens[b] exist; the others
  *             of o and lse are left as they are.
  *   causal    != 0: row i sees tokens j <= n - m + i (the m rows are the last of the n
@@ -590,7 +591,7 @@ sfa_status sfa_cache_read(const sfa_rows_desc *desc, const sfa_cache *cache, con
  *   max_kv    an upper bound of the n of this call, by which the keys are cut into ranges
  *             that run side by side (0: table_len * page_len).  It sets the speed, never the
  *             result's meaning: longer caches are attended in full all the same.
- *   workspace device memory of sfa_forward_cache_workspace bytes, 256-byte aligned, scratch
+ *   workspace device memory of sfa_forward_cache_workspace bytes for this descriptor, 256-byte aligned, scratch
  *             (NULL where that is 0).  Calls that can overlap need one each.
  * Keys at and behind n, and other pages, may hold anything.  An n outside
  * [0, table_len * page_len] or a page number outside the pool is reported as

@@ -7,7 +7,7 @@ import torch
 
 from oracle import cache as C
 
-from cache_helpers import empty_pool, f64, gather, random_pool, strided, tables
+from cache_helpers import empty_pool, f64, gather, pool_values, random_pool, strided, tables
 from gpu_helpers import sfa
 
 pytestmark = pytest.mark.gpu
@@ -450,3 +450,63 @@ def test_calls_of_two_threads():
             for r in got:
                 for a, b in zip(w, r):
                     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+DEALT = [  # B, Hk, G, L, d, kv, page_len, causal, flags, max_kv as a share of kv
+    (2, 8, 1, 1, 64, 30000, 64, False, ROWS, 1.0),
+    (2, 8, 2, 5, 128, 30000, 40, True, ROWS, 1.0),
+    (37, 3, 1, 1, 64, 4300, 16, False, ROWS, 1.0),
+    (3, 11, 1, 100, 64, 2000, 16, True, TILES, 1.0),
+    (3, 11, 1, 70, 128, 1500, 40, False, TILES, 0.3),
+    (2, 2, 3, 290, 128, 3000, 64, True, TILES, 1.0),
+    (1, 5, 1, 600, 64, 2500, 200, True, TILES, 1.5),
+    (64, 1, 1, 130, 64, 700, 16, False, TILES, 1.0),
+]
+
+
+@pytest.mark.parametrize("how", ["one", "spread", "nothing", "all but one", "twos"])
+@pytest.mark.parametrize("case", DEALT)
+def test_uneven_caches_share_the_gpu(case, how):
+    """Ranges dealt out by the lengths on the device: a long cache among short ones, empty ones,
+    bounds that are too small, more caches than a warp has lanes, several row tiles."""
+    B, Hk, G, L, d, kv, P, causal, flags, share = case
+    m, g = sfa(), np.random.default_rng(kv + L)
+    cache = random_pool(g, m, 50, 1, P, d)
+    table = g.integers(0, 50, (B, Hk, -(-kv // P))).astype(np.int32)
+    n = {"one": np.full((B, Hk), kv // 9), "spread": g.integers(0, kv + 1, (B, Hk)), "nothing": np.zeros((B, Hk)),
+         "all but one": np.full((B, Hk), kv), "twos": kv // (1 + np.arange(B * Hk).reshape(B, Hk) % 2)}[how].astype(np.int32)
+    n[-1, -1] = {"one": kv, "all but one": 1}.get(how, n[-1, -1])
+    q = torch.from_numpy(g.standard_normal((B, Hk * G, L, d))).bfloat16()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, l = m.forward_cache(q.cuda(), cache, torch.from_numpy(table).cuda(), torch.from_numpy(n).cuda(), causal=causal,
+                           max_kv=max(1, int(share * kv)), dev_status=status, debug_flags=flags)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    empty = torch.from_numpy(np.repeat(n == 0, G, 1))
+    assert (o.cpu()[empty] == 0).all() and torch.isneginf(l.cpu()[empty]).all() and torch.isfinite(o).all()
+    (kc, ke), (vc, ve) = pool_values(cache)
+    k_all, v_all = C.dequantise(kc, ke)[:, 0], C.dequantise(vc, ve)[:, 0]
+    caches = [(b, h) for b in range(B) for h in range(Hk)]
+    some = caches if kv * L < 100000 else caches[:3] + caches[-3:]
+    for b, h in some[:40] + some[-1:]:
+        at = table[b, h].astype(int)
+        k, v = (x[at].reshape(-1, d)[: n[b, h]] for x in (k_all, v_all))
+        for i in range(G):
+            check(o[b, h * G + i], l[b, h * G + i], f64(q[b, h * G + i]), k, v, 1 / math.sqrt(d), causal)
+
+
+@pytest.mark.parametrize("B,Hk,L", [(1, 12, 40), (2, 3, 300), (1, 16, 1)])
+@pytest.mark.parametrize("shape", ["heads", "shared", "one"])
+def test_workspace_bytes_are_those_of_the_call(B, Hk, L, shape):
+    m, g = sfa(), np.random.default_rng(L)
+    cache = random_pool(g, m, 40, 1, 64, 64)
+    table = torch.from_numpy(g.integers(0, 40, (B, Hk, 600)).astype(np.int32)).cuda()
+    n = torch.from_numpy(g.integers(2000, 600 * 64, (B, Hk)).astype(np.int32)).cuda()
+    n = {"heads": n, "shared": n[:, :1].contiguous(), "one": n[:, 0].contiguous()}[shape]
+    q = torch.from_numpy(g.standard_normal((B, Hk, L, 64))).bfloat16().cuda()
+    size = m.forward_cache_workspace_bytes(q, cache, table, n)
+    ws = torch.full((size + 256,), 0xff, dtype=torch.uint8, device="cuda")
+    o1, l1 = m.forward_cache(q, cache, table, n, workspace=ws[:size])
+    o2, l2 = m.forward_cache(q, cache, table, n)
+    torch.cuda.synchronize()
+    assert size > 0 and torch.equal(o1, o2) and torch.equal(l1, l2) and (ws[size:] == 0xff).all()
