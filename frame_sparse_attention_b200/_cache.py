@@ -137,7 +137,7 @@ def cache_append(cache: FrameCache, q, k, v, table, start, lens=None, rope: Rope
                  dev_status=None, stream=None):
     """qk_norm_rope of q and k, and cache_write of those keys and v, in one pass (the bf16 keys
     are not written).  Arguments as theirs; returns q_out.  Padding rows of q_out (from lens[b]
-    on) are left as they are."""
+    on) are left as they are (zero where it is allocated here)."""
     return (_bind or _load_bind()).cache_append(cache, q, k, v, table, start, lens, rope, positions, q_weight, k_weight, eps,
                                                 layout, q_out, dev_status, stream)
 
@@ -162,7 +162,8 @@ def forward_cache(q, cache: FrameCache, table, kv_lens, causal: bool = False, q_
     """Attention of new tokens over the cache: (O bf16 like q, LSE fp32 [B, H, Lq]).
 
     q bf16 [B, H, Lq, d]; kv_lens int32 [B] or [B, H_kv]: logical tokens [0, n) are the keys and
-    values.  q_lens int32 [B]: rows from there on are padding, left as they are.  causal: the
+    values.  q_lens int32 [B]: rows from there on are padding, left as they are (O = 0 and LSE = -inf
+    where the outputs are allocated here).  causal: the
     rows are the last of the n tokens and see none behind themselves.  max_kv: an upper bound of
     kv_lens, for the split of the work (0: all that the table can hold).  workspace: a uint8
     tensor of forward_cache_workspace_bytes (allocated here when not given).  H_kv: key heads,

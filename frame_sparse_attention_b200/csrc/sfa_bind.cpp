@@ -15,7 +15,9 @@
 
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
+#include <ATen/ops/full.h>
 #include <ATen/ops/zeros.h>
+#include <ATen/ops/zeros_like.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -270,12 +272,13 @@ void launch(int dev, const char *what, F fn)
     check(status, what);
 }
 
-// An output: the caller's, or a new one like `t`.
-Tensor output(const char *name, PyObject *o, const Tensor &t)
+// An output: the caller's, or a new one like `t`.  padded: rows from a sequence's length on are not
+// written, so a new one starts as zeros (in the caller's they stay as they are).
+Tensor output(const char *name, PyObject *o, const Tensor &t, bool padded = false)
 {
     if (given(o)) return tensor(name, o);
     const NoGil free;
-    return at::empty_like(t);
+    return padded ? at::zeros_like(t) : at::empty_like(t);
 }
 
 float eps_of(PyObject *o) { return given(o) ? (float)number(o) : -1.f; }
@@ -387,7 +390,7 @@ PyObject *cache_append(PyObject *, PyObject *const *x, Py_ssize_t n)
     desc.eps = eps_of(x[11]);
     const void *q = rows("q", tq, dev, s, desc.q_stride), *k = rows("k", tk, dev, shape, desc.k_stride);
     const void *v = rows("v", tensor("v", x[3]), dev, shape, desc.v_stride);
-    const Tensor q_out = output("q_out", x[13], tq);
+    const Tensor q_out = output("q_out", x[13], tq, given(x[6]));
     void *qo = rows("q_out", q_out, dev, s, desc.q_out_stride);
     const sfa_cache cache = cache_desc(x[0], x[4], dev, B, H_kv, d);
     const int32_t *start = per_head("start", x[5], dev, B, H_kv, desc.start_stride), *lens = lengths("lens", x[6], dev, B);
@@ -496,7 +499,8 @@ PyObject *forward_cache(PyObject *, PyObject *const *x, Py_ssize_t n)
     const int64_t B = s[0], H = s[1], Lq = s[2], d = s[3], per_row[3] = {B, H, Lq};
     sfa_cache_attn_desc desc = {};
     const void *q = rows("q", tq, dev, s, desc.q_stride);
-    const Tensor out = output("out", x[8], tq);
+    const bool padded = given(x[5]);
+    const Tensor out = output("out", x[8], tq, padded);
     void *o = rows("out", out, dev, s, desc.o_stride);
     Tensor lse;
     if (given(x[9])) {
@@ -506,7 +510,8 @@ PyObject *forward_cache(PyObject *, PyObject *const *x, Py_ssize_t n)
                           "lse must be a contiguous fp32 tensor ", IntArrayRef(per_row, 3), " on device ", dev);
     } else {
         const NoGil free;
-        lse = at::empty(per_row, tq.options().dtype(at::kFloat));
+        const auto fp32 = tq.options().dtype(at::kFloat);
+        lse = padded ? at::full(per_row, -INFINITY, fp32) : at::empty(per_row, fp32);
     }
     const int64_t H_kv = key_heads(x[11], x[1], x[2], x[3]);
     const sfa_cache cache = cache_desc(x[1], x[2], dev, B, H_kv, d);
