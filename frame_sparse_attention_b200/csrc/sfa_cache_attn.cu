@@ -1441,6 +1441,16 @@ struct Plan {
     int64_t ctas;
 };
 
+// Bytes of the ranges' partial results (fp32 O and LSE of every row, n_split times).
+size_t part_bytes(const sfa_cache_attn_desc *d, int n_split)
+{
+    if (n_split == 1) return 0;
+    const size_t rows = (size_t)d->B * d->H * d->Lq;
+    return (n_split * rows * (d->d + 1) * sizeof(float) + 255) / 256 * 256;
+}
+
+constexpr size_t PART_BYTES_MAX = (size_t)512 << 20;  // that a plan asks for, at most
+constexpr double PART_BYTES_L2 = 96e6;                // that stay in the L2 cache (126 MB) between the kernels
 constexpr int FEW_ROWS = 32;
 constexpr double DEALT_STEPS = 6.0;  // key steps a CTA, below which the lengths are not dealt out
 
@@ -1471,21 +1481,34 @@ Plan plan_of(const sfa_cache_attn_desc *d, const sfa_cache *c)
     const int64_t units = (int64_t)d->B * d->H_kv * p.row_tiles;
     const int64_t steps = std::max<int64_t>(1, (kv + step_keys - 1) / step_keys);
     // The number of ranges per unit, by the steps that the launch takes: a range takes its own
-    // steps and a fixed start and end, and the join of k ranges a little.  The lengths are on
+    // steps and a fixed start and end, the join of k ranges a little, and partial results beyond
+    // the L2 cache go out to memory and come back (a step is some 2.7 us, 2.0 at d = 64).  The lengths are on
     // the device, so the mean of two cases is taken: all caches as long as the bound (whole
     // waves of equal ranges), and lengths spread between half of it and all of it (three
     // quarters of the ranges, which then even out but for the last one's end).  Measured, one
     // token, 96 units of 128 steps, k = 3, 6, 9, 12, 18: 99, 111, 92, 101, 101 us at one
     // length and 94, 100, 86, 87, 82 at uneven ones; 32 units, k = 9, 13, 18: 42, 37, 46 and 40, 37, 34.
+    // Many rows are seldom worth their partial results.  d = 128, k = 1, 2, 3, ms at one length and
+    // at uneven ones: 64 heads on 8, 25600 rows over 65536, 58.3, 61.5, 62.2 and 43.7, 46.0, 47.0 (1.69 GB of
+    // workspace for k = 2); 12 heads, 16384 over 8192, 1.03, 1.12, 1.15 and 0.74, 0.92, 0.92, over 65536
+    // 7.9, 7.5, 7.3 and 5.6, 5.6, 5.5; 4680 over 20280, 0.85, 0.87, 0.78 and 0.70, 0.60, 0.63.  Without
+    // the bytes' term the first two of these took k = 2; with all bytes in it, those that stay in L2 too,
+    // 1560 over 8192, 12 heads on 4, d = 64, took 3 ranges, not 5, and 107 us instead of 98.  Beyond
+    // PART_BYTES_MAX, where k = 1 needs no memory at all, ranges gain 5 % at most (12 heads, 25600
+    // over 65536: 11.3 and 11.9).
     const double slots = (double)attn_sms() * (p.tiles ? 1 : FR_CTAS);
     const double fixed = p.tiles ? 5.0 : 2.0;
+    const double step_bytes = d->d == 128 ? 17.5e6 : 13e6;  // of HBM traffic in the time of a step
     double best = 1e300;
     p.n_split = 1;
     for (int64_t k = 1; k <= MAX_SPLIT && k <= steps; ++k) {
+        if (part_bytes(d, (int)k) > PART_BYTES_MAX) break;
         const double piece = (double)((steps + k - 1) / k) + fixed, waves = units * k / slots;
         const double even = std::ceil(waves) * piece;
         const double uneven = waves <= 1.0 ? piece : (0.75 * waves + 0.5) * piece;
-        const double cost = 0.5 * (even + uneven) + (k > 1 ? 1.5 + 0.05 * k : 0.0);
+        const double out = std::max(0.0, (double)part_bytes(d, (int)k) - PART_BYTES_L2);
+        const double join = k > 1 ? 1.5 + 0.05 * k + 2.0 * out / step_bytes : 0.0;
+        const double cost = 0.5 * (even + uneven) + join;
         if (cost < best) {
             best = cost;
             p.n_split = (int)k;
@@ -1568,13 +1591,6 @@ sfa_status launch_few_rows(const ChunkArgs &a, const sfa_cache *c, unsigned grid
         return c->d == 128 ? launch_rows_attn<128, true>(a, tk, tv, grid, s) : launch_rows_attn<64, true>(a, tk, tv, grid, s);
     }
     return c->d == 128 ? launch_rows_attn<128, false>(a, tk, tv, grid, s) : launch_rows_attn<64, false>(a, tk, tv, grid, s);
-}
-
-size_t part_bytes(const sfa_cache_attn_desc *d, int n_split)
-{
-    if (n_split == 1) return 0;
-    const size_t rows = (size_t)d->B * d->H * d->Lq;
-    return (n_split * rows * (d->d + 1) * sizeof(float) + 255) / 256 * 256;
 }
 
 }  // namespace

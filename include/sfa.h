@@ -591,8 +591,8 @@ sfa_status sfa_cache_read(const sfa_rows_desc *desc, const sfa_cache *cache, con
  *   max_kv    an upper bound of the n of this call, by which the keys are cut into ranges
  *             that run side by side (0: table_len * page_len).  It sets the speed, never the
  *             result's meaning: longer caches are attended in full all the same.
- *   workspace device memory of sfa_forward_cache_workspace bytes for this descriptor, 256-byte aligned, scratch
- *             (NULL where that is 0).  Calls that can overlap need one each.
+ *   workspace device memory of sfa_forward_cache_workspace bytes for this descriptor (512 MB at most),
+ *             256-byte aligned, scratch (NULL where that is 0).  Calls that can overlap need one each.
  * Keys at and behind n, and other pages, may hold anything.  An n outside
  * [0, table_len * page_len] or a page number outside the pool is reported as
  * SFA_ERR_BAD_SET in dev_status; the rows of that (b, hk) are then unspecified, and nothing
