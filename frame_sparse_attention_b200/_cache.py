@@ -12,6 +12,8 @@ from __future__ import annotations
 import importlib
 import math
 import os
+import re
+import sys
 from typing import NamedTuple
 
 import torch
@@ -94,9 +96,19 @@ def _load_bind():
     global _bind
     load()  # the library that it calls
     path = os.path.join(_PKG, "_bind.so")
+    how = "build it with `python -m frame_sparse_attention_b200.build`"
     if not os.path.exists(path):
-        raise RuntimeError(f"{path} is missing: build it with `python -m frame_sparse_attention_b200.build`")
-    _bind = importlib.import_module("._bind", __package__)
+        raise RuntimeError(f"{path} is missing: {how}")
+    try:
+        module = importlib.import_module("._bind", __package__)
+    except ImportError as e:
+        raise RuntimeError(f"{path} does not load ({e}): {how}") from e
+    # objects of another PyTorch or interpreter may be laid out otherwise
+    torch_version = re.match(r"\d+\.\d+\.\d+", torch.__version__)
+    have = f"torch {torch_version.group() if torch_version else torch.__version__}, python {sys.version_info[0]}.{sys.version_info[1]}"
+    if module.built_for != have:
+        raise RuntimeError(f"{path} was built for {module.built_for}, this is {have}: {how}")
+    _bind = module
     return _bind
 
 

@@ -5,8 +5,9 @@
 Each csrc/*.cu is compiled to an object under _build/ (rebuilt when it or a header
 changed), then linked into frame_sparse_attention_b200/libsfa.so with the CUDA
 runtime linked statically; csrc/sfa_bind.cpp, the binding of the 8-bit frame cache's calls,
-is built with the C++ compiler against PyTorch's headers and libsfa.so.  No GPU is needed to
-build.
+is built with the C++ compiler against PyTorch's headers and libsfa.so (again when PyTorch or
+the interpreter changed: _build/sfa_bind.built_for says what it was built for).  No GPU is
+needed to build.
 """
 from __future__ import annotations
 
@@ -26,6 +27,7 @@ OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsfa.so")
 BIND = os.path.join(PKG, "_bind.so")
 BIND_SRC = os.path.join(CSRC, "sfa_bind.cpp")
+BIND_BUILT_FOR = os.path.join(OBJDIR, "sfa_bind.built_for")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -42,10 +44,25 @@ def _newest_header() -> float:
     return max((os.path.getmtime(h) for h in hdrs), default=0.0)
 
 
+def _bind_target() -> str:
+    """What _bind.so's object layout depends on beside its source: PyTorch, its C++ ABI, the interpreter."""
+    import torch
+    return (f"torch {torch.__version__} cxx11abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} "
+            f"python {sysconfig.get_config_var('SOABI')}")
+
+
+def _bind_fresh(target: str) -> bool:
+    if not (os.path.exists(BIND) and os.path.exists(BIND_BUILT_FOR)):
+        return False
+    with open(BIND_BUILT_FOR) as f:
+        built_for = f.read()
+    return built_for == target and os.path.getmtime(BIND) >= max(os.path.getmtime(BIND_SRC), _newest_header())
+
+
 def _build_bind(nvcc: str, force: bool) -> None:
     """_bind.so, with torch's own libraries as they are loaded already by `import torch`."""
-    newest = max(os.path.getmtime(BIND_SRC), _newest_header())
-    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= newest:
+    target = _bind_target()
+    if not force and _bind_fresh(target):
         return
     import torch
     from torch.utils.cpp_extension import include_paths, library_paths
@@ -58,6 +75,8 @@ def _build_bind(nvcc: str, force: bool) -> None:
                            *(f"-L{i}" for i in library_paths()), f"-L{PKG}", "-l:libsfa.so", "-Wl,-rpath,$ORIGIN",
                            "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
     os.replace(tmp, BIND)
+    with open(BIND_BUILT_FOR, "w") as f:
+        f.write(target)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:

@@ -11,6 +11,7 @@
 #include <cstdint>
 #include <cstring>
 #include <initializer_list>
+#include <string>
 #include <utility>
 
 #include <ATen/ops/empty.h>
@@ -22,6 +23,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/headeronly/version.h>
 
 #include "sfa.h"
 
@@ -574,6 +576,14 @@ PyMODINIT_FUNC PyInit__bind()
             Py_DECREF(m);
             return nullptr;
         }
+    }
+    // what _cache.py compares with the versions that it runs under
+    const std::string built_for = "torch " + std::to_string(TORCH_VERSION_MAJOR) + "." + std::to_string(TORCH_VERSION_MINOR) +
+                                  "." + std::to_string(TORCH_VERSION_PATCH) + ", python " +
+                                  std::to_string(PY_MAJOR_VERSION) + "." + std::to_string(PY_MINOR_VERSION);
+    if (PyModule_AddStringConstant(m, "built_for", built_for.c_str()) < 0) {
+        Py_DECREF(m);
+        return nullptr;
     }
     return m;
 }
