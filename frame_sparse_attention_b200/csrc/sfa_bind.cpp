@@ -283,7 +283,14 @@ Tensor output(const char *name, PyObject *o, const Tensor &t, bool padded = fals
     return padded ? at::zeros_like(t) : at::empty_like(t);
 }
 
-float eps_of(PyObject *o) { return given(o) ? (float)number(o) : -1.f; }
+// The descriptor's eps: below 0 it stands for no norm, which a caller asks for with None.
+float eps_of(PyObject *o)
+{
+    if (!given(o)) return -1.f;
+    const double eps = number(o);
+    TORCH_CHECK_VALUE(!(eps < 0.0), "expected eps >= 0, or None for no norm: ", eps);
+    return (float)eps;
+}
 
 PyObject *pair(PyObject *a, PyObject *b)  // takes both references
 {
