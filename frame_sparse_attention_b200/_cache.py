@@ -63,14 +63,17 @@ def rope_table(axis_dims, theta: float = 10000.0, scaling: str = "none", factor:
     scaling, for contexts ``factor`` times longer than trained: "linear" divides the
     frequencies by factor; "ntk" raises theta to theta * factor^(n/(n-2)); "yarn" (Peng et al.
     2023) divides those that turn less than beta_slow times over ``original_len`` positions,
-    keeps those that turn more than beta_fast times, blends the ones between, and scales
-    rotated values by 0.1 ln(factor) + 1."""
+    keeps those that turn more than beta_fast times, blends the ones between linearly in their
+    number of turns, as the paper has it, and scales rotated values by 0.1 ln(factor) + 1.
+    (Many published checkpoints blend linearly in the pair's index instead, between bounds
+    rounded to whole indices: a model trained so needs a RopeTable of its own frequencies.)"""
     dims = [int(n) for n in axis_dims]
     _require(0 < len(dims) <= ROPE_MAX_AXES and all(n >= 0 and n % 2 == 0 for n in dims) and sum(dims) > 0,
              "expected 1 to 4 even axis dimensions")
     _require(scaling in ("none", "linear", "ntk", "yarn"), "expected scaling in (none, linear, ntk, yarn)")
-    _require(factor > 0 and theta > 0, "expected factor > 0 and theta > 0")
+    _require(0 < factor < math.inf and 0 < theta < math.inf, "expected finite factor > 0 and theta > 0")
     _require(scaling != "yarn" or original_len > 0, "yarn needs original_len")
+    _require(scaling != "yarn" or beta_fast > beta_slow, "yarn needs beta_fast > beta_slow")
     freq, scale = [], 1.0
     for n in dims:
         base = theta * factor ** (n / (n - 2)) if scaling == "ntk" and n > 2 else theta

@@ -17,3 +17,24 @@ def test_a_negative_eps_is_no_request_for_no_norm(sfa):  # noqa: F811
     for eps in (None, 0.0, -0.0, 1e-6):  # (refused for what the tensors are)
         with pytest.raises(ValueError, match="CUDA"):
             sfa.qk_norm_rope(q, eps=eps)
+
+
+def test_rope_tables_without_a_meaning(sfa):  # noqa: F811
+    inf, nan = float("inf"), float("nan")
+    yarn = dict(scaling="yarn", factor=2.0, original_len=64)
+    for kw in (dict(factor=inf, scaling="linear"), dict(factor=nan), dict(theta=inf), dict(theta=nan), dict(yarn, beta_fast=1.0),
+               dict(yarn, beta_fast=1.0, beta_slow=32.0), dict(yarn, beta_slow=nan)):
+        with pytest.raises(ValueError):
+            sfa.rope_table((64,), device="cpu", **kw)
+
+
+def test_yarn_blends_by_turns(sfa):  # noqa: F811
+    """Pair by pair from the paper's formula."""
+    import math
+    n, L, factor, fast, slow = 64, 4096, 8.0, 32.0, 1.0
+    t = sfa.rope_table((n,), scaling="yarn", factor=factor, original_len=L, device="cpu").inv_freq.tolist()
+    for i, f in enumerate(t):
+        base = 10000.0 ** (-2 * i / n)
+        turns = L * base / (2 * math.pi)
+        gamma = 0.0 if turns < slow else 1.0 if turns > fast else (turns - slow) / (fast - slow)
+        assert math.isclose(f, (1 - gamma) * base / factor + gamma * base, rel_tol=1e-14)
