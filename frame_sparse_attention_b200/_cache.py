@@ -136,7 +136,7 @@ def qk_norm_rope(q, k=None, rope: RopeTable | None = None, positions=None, q_wei
     q bf16 [B, H, L, d], k bf16 [B, H_kv, L, d] (either may be None); weights fp32 [d] or None
     (ones); eps None: no norm.  rope None: no rotation, else positions int32 [B, L, axes]
     (or [L, axes], shared by the batch).  Returns (q_out, k_out), bf16, None where there was no
-    input; an output may be its input (in place)."""
+    input; an output may be its input (in place, under the same strides) and overlap nothing else."""
     return (_bind or _load_bind()).qk_norm_rope(q, k, rope, positions, q_weight, k_weight, eps, layout, q_out, k_out, stream)
 
 

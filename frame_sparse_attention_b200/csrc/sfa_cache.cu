@@ -566,6 +566,16 @@ bool weights_ok(const float *q, const float *k)
 
 bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+// An output at its input's address is written row by row as the rows are read, which takes the same
+// rows at the same places.
+bool in_place_ok(const void *in, const void *out, const int64_t *si, const int64_t *so, int64_t B, int64_t heads, int64_t L)
+{
+    const int64_t n[3] = {B, heads, L};
+    for (int i = 0; i < 3; ++i)
+        if (in == out && n[i] > 1 && si[i] != so[i]) return false;
+    return true;
+}
+
 sfa_status check_rows(const sfa_rows_desc *d)
 {
     if (!d || d->B < 0 || d->L < 0) return SFA_ERR_INVALID_ARG;
@@ -707,6 +717,10 @@ extern "C" sfa_status sfa_qk_norm_rope(const sfa_rows_desc *d, const sfa_rope *r
         return SFA_ERR_INVALID_ARG;
     if (k && (!rows_stride_ok(d->k_stride, d->B, d->H_kv, d->L) || !rows_stride_ok(d->k_out_stride, d->B, d->H_kv, d->L)))
         return SFA_ERR_INVALID_ARG;
+    if (q && k && (q_out == k || k_out == q || q_out == k_out)) return SFA_ERR_INVALID_ARG;
+    if ((q && !in_place_ok(q, q_out, d->q_stride, d->q_out_stride, d->B, d->H, d->L)) ||
+        (k && !in_place_ok(k, k_out, d->k_stride, d->k_out_stride, d->B, d->H_kv, d->L)))
+        return SFA_ERR_INVALID_ARG;
     RowsArgs a = {};
     a.B = d->B;
     a.H = d->H;
@@ -772,6 +786,8 @@ extern "C" sfa_status sfa_cache_append(const sfa_rows_desc *d, const sfa_rope *r
     if (!rows_stride_ok(d->q_stride, d->B, d->H, d->L) || !rows_stride_ok(d->q_out_stride, d->B, d->H, d->L) ||
         !rows_stride_ok(d->k_stride, d->B, d->H_kv, d->L) || !rows_stride_ok(d->v_stride, d->B, d->H_kv, d->L))
         return SFA_ERR_INVALID_ARG;
+    if (q_out == k || q_out == v || !in_place_ok(q, q_out, d->q_stride, d->q_out_stride, d->B, d->H, d->L))
+        return SFA_ERR_INVALID_ARG;
     RowsArgs a = {};
     a.B = d->B;
     a.H = d->H;
@@ -798,7 +814,7 @@ extern "C" sfa_status sfa_cache_read(const sfa_rows_desc *d, const sfa_cache *ca
     if (d->B == 0 || d->L == 0) return SFA_OK;
     st = check_cache_rows(d, cache, start);
     if (st != SFA_OK) return st;
-    if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return SFA_ERR_INVALID_ARG;
+    if (!k_out || !v_out || k_out == v_out || !aligned16(k_out) || !aligned16(v_out)) return SFA_ERR_INVALID_ARG;
     if (!rows_stride_ok(d->k_out_stride, d->B, d->H_kv, d->L) || !rows_stride_ok(d->v_out_stride, d->B, d->H_kv, d->L))
         return SFA_ERR_INVALID_ARG;
     ReadArgs a = {};

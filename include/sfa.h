@@ -545,7 +545,8 @@ typedef struct {
  *   y = x / sqrt(mean(x^2) + eps) * weight  (per head row; weight fp32 [d], 16-byte aligned,
  *   or NULL = ones; no norm with eps < 0), then the rotation (rope NULL: none), in fp32, rounded to bf16 once.
  *   (The sum of squares is fp32 too: rows whose elements pass 1e19 give 0.)
- * q or k may be NULL (with its output).  q_out / k_out may be q / k themselves (same strides).
+ * q or k may be NULL (with its output).  q_out / k_out may be q / k themselves (same strides, else
+ * SFA_ERR_INVALID_ARG); no output may overlap any other argument.
  */
 sfa_status sfa_qk_norm_rope(const sfa_rows_desc *desc, const sfa_rope *rope, const void *q, const void *k,
                             const float *q_weight, const float *k_weight, void *q_out, void *k_out,

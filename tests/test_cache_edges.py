@@ -38,3 +38,37 @@ def test_yarn_blends_by_turns(sfa):  # noqa: F811
         turns = L * base / (2 * math.pi)
         gamma = 0.0 if turns < slow else 1.0 if turns > fast else (turns - slow) / (fast - slow)
         assert math.isclose(f, (1 - gamma) * base / factor + gamma * base, rel_tol=1e-14)
+
+
+def _views():
+    from test_cache_abi import _structs
+    rows, cache, rope = _structs()  # contiguous [2, 4, 8, 64] and [2, 2, 8, 64]
+    return rows, cache, rope
+
+
+def test_outputs_at_an_inputs_address(sfa):  # noqa: F811
+    """In place means the same rows at the same places; an output is nobody else's memory."""
+    import ctypes
+
+    from test_cache_abi import GOOD
+    lib, r = sfa.load(), ctypes.byref
+    a, b, c, x = (GOOD + (i << 16) for i in range(4))
+
+    def norm(rows, *args):
+        return lib.sfa_qk_norm_rope(r(rows), None, *args[:2], None, None, *args[2:], None)
+
+    def append(rows, q, k, v, q_out):
+        return lib.sfa_cache_append(r(rows), None, r(cache), q, k, v, None, None, q_out, GOOD, None, None, None)
+    for t, args in (("q", (a, None, a, None)), ("k", (None, a, None, a))):
+        rows, cache, _ = _views()
+        for i, s in enumerate((4 * 8 * 64, 64, 4 * 64)):  # [B, L, heads, d] over the same memory
+            setattr(rows, f"{t}_out_stride{i}", s)
+        assert norm(rows, *args) == 1
+        if t == "q":
+            assert append(rows, a, b, c, a) == 1
+    rows, cache, _ = _views()
+    for args in ((a, b, b, x), (a, b, x, a), (a, b, x, x), (a, a, a, a)):
+        assert norm(rows, *args) == 1
+    for args in ((a, b, c, b), (a, b, c, c)):
+        assert append(rows, *args) == 1
+    assert lib.sfa_cache_read(r(rows), r(cache), GOOD, None, a, a, None, None) == 1
