@@ -36,7 +36,9 @@ class FrameCache(NamedTuple):
     """An 8-bit page pool: codes float8_e4m3fn [n_pages, heads, page_len, d] and scales
     float8_e8m0fnu [n_pages, heads, page_len, d/32] of the keys and the values.  heads is the
     number of key heads, or 1 for pages that belong to one head each (then every head has its
-    own row of the page table and can keep other frames than its neighbours)."""
+    own row of the page table and can keep other frames than its neighbours).  cache_write and
+    cache_append never store the formats' NaNs; in a pool filled otherwise they are read as
+    numbers (codes as 480, scales as 2^128)."""
     k: torch.Tensor
     k_scale: torch.Tensor
     v: torch.Tensor

@@ -489,6 +489,10 @@ sfa_status sfa_gdn_forward(const sfa_gdn_desc *desc, const void *q, const void *
  * precision, and c * 2^e is a bf16 number exactly: reading back adds no rounding, and the
  * attention sees the cache's own values.  A NaN is stored as 0 and an infinity as the
  * largest value of its sign, and both are reported as SFA_ERR_INVALID_ARG in dev_status.
+ * A cache filled otherwise holds what is written here too: the format's own NaNs are read as
+ * numbers, without a report (codes 0x7f and 0xff as 480 of their sign, a scale byte of 255 as
+ * 2^128), and where c * 2^e is no bf16 number (e outside [-124, 119]) it is rounded, to infinity
+ * above.
  */
 #define SFA_CACHE_BLOCK 32
 

@@ -44,3 +44,33 @@ def test_padded_rows_of_allocated_outputs(L):
     m.cache_append(m.cache_create(10, 64, d, heads=H), q, k, v, table, torch.zeros_like(lens), lens=rows, q_out=y2)
     for b, n in enumerate(rows.tolist()):
         assert (o2[b, :, n:] == 5).all() and (l2[b, :, n:] == 5).all() and (y2[b, :, n:] == 5).all()
+
+
+def test_nan_codes_and_scales_are_read_as_the_numbers_that_the_header_names():
+    """Alone in a row, so that the attention of one key gives the row itself."""
+    m, d = sfa(), 128
+    rows = torch.zeros(6, d, dtype=torch.uint8)
+    scale = torch.full((6, d // 32), 127, dtype=torch.uint8)
+    rows[0, 5], rows[1, 70], rows[2, 127] = 0x7f, 0xff, 0x7f
+    scale[2] = 200                     # 480 * 2^73
+    rows[3, 9], scale[3] = 0x01, 255   # 2^-9 * 2^128
+    rows[4, 9], scale[4] = 0x3c, 255   # 1.5 * 2^128: past bf16
+    rows[5, 9], scale[5] = 0x38, 1     # 2^-126
+    want = torch.zeros(6, d, dtype=torch.float64)
+    want[0, 5], want[1, 70], want[2, 127] = 480.0, -480.0, 480.0 * 2.0 ** 73
+    want[3, 9], want[4, 9], want[5, 9] = 2.0 ** 119, float("inf"), 2.0 ** -126
+    cache = m.cache_create(6, 1, d)
+    for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        c.view(torch.uint8).copy_(rows.reshape(6, 1, 1, d))
+        s.view(torch.uint8).copy_(scale.reshape(6, 1, 1, 4))
+    table = torch.arange(6, dtype=torch.int32, device="cuda").reshape(6, 1)
+    zero = torch.zeros(6, dtype=torch.int32, device="cuda")
+    k, v = m.cache_read(cache, table, zero, 1)
+    assert torch.equal(k[:, 0, 0].double().cpu(), want) and torch.equal(v[:, 0, 0].double().cpu(), want)
+    finite = [0, 1, 2]  # (magnitudes of 2^100 and more may overflow in a partial result)
+    for L, flags in ((1, m.SFA_DEBUG_CACHE_ROWS), (40, m.SFA_DEBUG_CACHE_TILES)):
+        q = torch.zeros(6, 1, L, d, dtype=torch.bfloat16, device="cuda")
+        o, l = m.forward_cache(q, cache, table, zero + 1, debug_flags=flags)
+        torch.cuda.synchronize()
+        assert torch.equal(o[finite].double().cpu(), want[finite][:, None, None].expand(3, 1, L, d))
+        assert (l[finite] == 0).all()
