@@ -304,8 +304,9 @@ __device__ __forceinline__ void skip_range(const ChunkArgs &a, const Unit &u, in
 // and the partial results are joined by their log-sum-exp.
 // What bounds it is issue: of some 1000 instructions for 32 keys of 128 elements 64 are matrix
 // instructions and 512 turn codes into bf16, at two warps and a half a scheduler that wait for
-// one another's results (51 % of the issue slots, the integer pipe 46 %).  Sixteen warps an SM instead
-// of twelve, with Q in shared memory to get by on 128 registers: 102 us instead of 86.
+// one another's results (55 % of the issue slots).  Sixteen warps an SM instead of twelve, with Q in
+// shared memory to get by on 128 registers: 102 us instead of 86.  17 to 32 rows are two row tiles,
+// which read and convert the cache twice (24 rows, 12 heads x 4 sequences over 8192: 47 us).
 constexpr int FR_WARPS = 4;
 constexpr int FR_ROWS = 16;              // the matrix instruction's rows
 constexpr int FR_STRETCH = 32;           // keys that a warp works on at a time
@@ -608,6 +609,9 @@ __global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
                 o[i][3] *= c1;
             }
         }
+        // P goes to bf16, the type of the product with V, off by 2^-8 of each probability at most, as
+        // sfa_forward does; in two bf16 parts it would double that product.  O's relative error is
+        // 0.0023 with it, 0.0016 where O alone is rounded.  The row sums are of the fp32 numbers.
         const float z0 = m0 == -INFINITY ? 0.f : -m0, z1 = m1 == -INFINITY ? 0.f : -m1;
         uint4 p[2];
 #pragma unroll
@@ -784,13 +788,15 @@ __global__ void __launch_bounds__(FR_WARPS * 32, FR_CTAS)
 // (with P in shared memory, as in the frame-list kernel, a key tile took 5600 cycles, 2200 of
 // them in the issue of 11 loads behind blocked stores).  So P stays in tensor memory, in the
 // columns of the S that it comes from or beside it, as the first operand of P V.
-// A unit takes 2.8 us a key tile at d = 128 (900 TFLOP/s; 2.0 us at d = 64), bound by the softmax
-// warps: 256 x 128 exponentials are 2000 cycles of an SM's special-function pipe, and the scores'
-// way out of tensor memory, the maximum, the scaling and the packing are issued beside them.  Its
-// start and end take as long as five key tiles at d = 128 (page lookups, queries, the first
-// conversions; the last product and the rows' way out).  The streaming chunk, 4680 rows of 12
-// heads over 20280 tokens and fewer: 0.389 TFLOP in 552 us, 704 TFLOP/s (with bf16 keys and values
-// in place sfa_forward takes 493).
+// A unit takes 2.8 us a key tile at d = 128 (900 TFLOP/s; 2.0 us at d = 64), some 5400 cycles, in
+// which no pipe is full: 256 x 128 exponentials are 2048 cycles of an SM's special-function pipe,
+// the four products about as many of the tensor cores, and half of the issue slots are used.
+// At d = 128, P lying in the columns of its S, a query tile's S waits for its P V of the key tile
+// before, and that for the softmax of 128 columns; with two query tiles under way this chain is the
+// time (the largest stall is the wait for tensor memory).  A unit's start and end take as long as
+// five key tiles at d = 128 (page lookups, queries, the first conversions; the last product and the
+// rows' way out).  The streaming chunk, 4680 rows of 12 heads over 20280 tokens and fewer: 0.389 TFLOP
+// in 552 us, 704 TFLOP/s (with bf16 keys and values in place sfa_forward takes 493).
 // warps 0-3: softmax of query tile A, 4-7: of B
 constexpr int CT_K_WARP = 8;              // 8-11: codes of K to bf16
 constexpr int CT_V_WARP = 12;             // 12-14: of V
@@ -1080,7 +1086,8 @@ __device__ __noinline__ void outgrown(uint32_t t_p, uint32_t t_o, int chunks, bo
 
 // One key tile of the online softmax for this thread's row (thread = TMEM lane) that sees the
 // columns [0, nv) of it (MASK; all of them otherwise), 32 columns at a time:
-// P = exp2(S * scale * log2e - m) as bf16 over the columns that S has been read from.  The first
+// P = exp2(S * scale * log2e - m) as bf16 (the type of the product with V; the row sums are of the
+// fp32 numbers) over the columns that S has been read from.  The first
 // tile takes its row maximum before; later a row keeps m until a chunk's probabilities sum to
 // more than 2^GROWTH (one above it, or enough of them).  m is -inf, and the row's
 // probabilities are 0, until the row has seen a key.  P V of the key tile before has to be

@@ -477,7 +477,13 @@ sfa_status sfa_gdn_forward(const sfa_gdn_desc *desc, const void *q, const void *
  * 8-bit frame cache: norm and rotation of queries and keys, writing, reading, attention
  * ------------------------------------------------------------------------------------
  * ("Head Forcing", §2: every head keeps its own cache of frames; "ISPA", §1: the cache of
- *  a streaming model is its largest tensor.)  A cache is a pool of pages of page_len rows
+ *  a streaming model is its largest tensor.)  For models that norm each head's own row and cache
+ * keys with all axes of their positions rotated.  A model that norms a token's whole projection
+ * does so before and passes eps < 0; keys cached with fewer axes rotated and re-encoded for each
+ * head when they are attended ("Head Forcing", §3) are read back with sfa_cache_read, rotated
+ * with sfa_qk_norm_rope and attended in bf16.
+ *
+ * A cache is a pool of pages of page_len rows
  * and a page table per (batch entry, key head): logical token j of (b, h) lies in row
  * j % page_len of page table[b * table_stride[0] + h * table_stride[1] + j / page_len].
  * A page is a frame (page_len = P) or any other number of tokens.
