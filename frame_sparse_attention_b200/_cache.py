@@ -185,7 +185,8 @@ def forward_cache(q, cache: FrameCache, table, kv_lens, causal: bool = False, q_
     kv_lens, for the split of the work (0: all that the table can hold).  workspace: a uint8
     tensor of forward_cache_workspace_bytes (allocated here when not given).  H_kv: key heads,
     where neither the pool, the table nor kv_lens says so.  Rows that see no key give O = 0,
-    LSE = -inf, so the result merges with other branches by lse_merge.  debug_flags: SFA_DEBUG_*
+    LSE = -inf, so the result merges with other branches by lse_merge.  out may be q (in place,
+    under the same strides).  debug_flags: SFA_DEBUG_*
     test hooks, 0 in normal use."""
     return (_bind or _load_bind()).forward_cache(q, cache, table, kv_lens, causal, q_lens, max_kv, scale, out, lse, workspace,
                                                  H_kv, dev_status, stream, timeout_us, debug_flags)

@@ -569,16 +569,6 @@ bool weights_ok(const float *q, const float *k)
 
 bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// An output at its input's address is written row by row as the rows are read, which takes the same
-// rows at the same places.
-bool in_place_ok(const void *in, const void *out, const int64_t *si, const int64_t *so, int64_t B, int64_t heads, int64_t L)
-{
-    const int64_t n[3] = {B, heads, L};
-    for (int i = 0; i < 3; ++i)
-        if (in == out && n[i] > 1 && si[i] != so[i]) return false;
-    return true;
-}
-
 sfa_status check_rows(const sfa_rows_desc *d)
 {
     if (!d || d->B < 0 || d->L < 0) return SFA_ERR_INVALID_ARG;

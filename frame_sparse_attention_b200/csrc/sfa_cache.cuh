@@ -66,6 +66,17 @@ inline bool rows_stride_ok(const int64_t *s, int64_t B, int64_t heads, int64_t L
     return true;
 }
 
+// An output at its input's address is written as the rows there have been read, which takes the
+// same rows at the same places.
+inline bool in_place_ok(const void *in, const void *out, const int64_t *si, const int64_t *so, int64_t B, int64_t heads,
+                        int64_t L)
+{
+    const int64_t n[3] = {B, heads, L};
+    for (int i = 0; i < 3; ++i)
+        if (in == out && n[i] > 1 && si[i] != so[i]) return false;
+    return true;
+}
+
 __device__ __forceinline__ void report_status(int32_t *status, int32_t code)
 {
     if (status) atomicCAS(status, 0, code);

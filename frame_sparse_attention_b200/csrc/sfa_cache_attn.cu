@@ -1630,7 +1630,8 @@ extern "C" sfa_status sfa_forward_cache(const sfa_cache_attn_desc *d, const sfa_
     if (st != SFA_OK) return st;
     if (!q || !o || !lse || !kv_lens || reinterpret_cast<uintptr_t>(q) % 16 || reinterpret_cast<uintptr_t>(o) % 16)
         return SFA_ERR_INVALID_ARG;
-    if (!rows_stride_ok(d->q_stride, d->B, d->H, d->Lq) || !rows_stride_ok(d->o_stride, d->B, d->H, d->Lq))
+    if (!rows_stride_ok(d->q_stride, d->B, d->H, d->Lq) || !rows_stride_ok(d->o_stride, d->B, d->H, d->Lq) ||
+        !in_place_ok(q, o, d->q_stride, d->o_stride, d->B, d->H, d->Lq))
         return SFA_ERR_INVALID_ARG;
     const Plan p = plan_of(d, cache);
     if (p.ctas >= ((int64_t)1 << 31)) return SFA_ERR_INVALID_ARG;

@@ -591,6 +591,7 @@ sfa_status sfa_cache_read(const sfa_rows_desc *desc, const sfa_cache *cache, con
  * Attention of a chunk of new tokens over the cache ("Head Forcing", §2: the chunk attends
  * each head's own cache; "LVSA", §2: softmax attention with its log-sum-exp).
  *   q, o      bf16 [B][H][Lq][d], strides in the descriptor; head h reads key head h / (H / H_kv).
+ *             o may be q itself (same strides, else SFA_ERR_INVALID_ARG) and overlap nothing else.
  *   kv_lens   device int32, n = kv_lens[b * len_stride[0] + hk * len_stride[1]]: the keys and
  *             values are logical tokens [0, n) of (b, hk).  n = 0 gives O = 0, LSE = -inf.
  *             (B = 1 with len_stride[1] = 0, one length for all, spares the look at the others.)

@@ -72,3 +72,12 @@ def test_outputs_at_an_inputs_address(sfa):  # noqa: F811
     for args in ((a, b, c, b), (a, b, c, c)):
         assert append(rows, *args) == 1
     assert lib.sfa_cache_read(r(rows), r(cache), GOOD, None, a, a, None, None) == 1
+
+
+def test_attention_output_at_the_queries_address(sfa):  # noqa: F811
+    from test_cache_abi import GOOD, _attn, _attn_call, _structs
+    _, cache, _ = _structs()
+    d = _attn(sfa)  # contiguous [2, 4, 8, 64]
+    for i, s in enumerate((4 * 8 * 64, 64, 4 * 64)):
+        setattr(d, f"o_stride{i}", s)
+    assert _attn_call(sfa, d, cache, q=GOOD, o=GOOD) == 1

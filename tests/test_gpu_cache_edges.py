@@ -74,3 +74,19 @@ def test_nan_codes_and_scales_are_read_as_the_numbers_that_the_header_names():
         torch.cuda.synchronize()
         assert torch.equal(o[finite].double().cpu(), want[finite][:, None, None].expand(3, 1, L, d))
         assert (l[finite] == 0).all()
+
+
+@pytest.mark.parametrize("L,flags", [(1, 4), (20, 4), (100, 8), (300, 8)])
+@pytest.mark.parametrize("kv", [100, 4000])
+def test_attention_in_place(L, flags, kv):
+    """O over its own queries: each is read before its row is written, keys in one range or several."""
+    m, g = sfa(), np.random.default_rng(L)
+    cache = random_pool(g, m, 20, 2, 200, 64)
+    table = torch.arange(20, dtype=torch.int32, device="cuda").reshape(1, 20)
+    lens = torch.tensor([kv], dtype=torch.int32, device="cuda")
+    q = torch.from_numpy(g.standard_normal((1, L, 6, 64))).bfloat16().cuda().transpose(1, 2)
+    args = dict(causal=True, max_kv=kv, debug_flags=flags)
+    o, l = m.forward_cache(q, cache, table, lens, **args)
+    o2, l2 = m.forward_cache(q, cache, table, lens, out=q, **args)
+    torch.cuda.synchronize()
+    assert o2 is q and torch.equal(o2, o) and torch.equal(l2, l)
